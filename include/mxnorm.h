@@ -442,6 +442,18 @@ int mxnorm_abi_version(void);
 int mxnorm_tiled_wait_drill(const void* x, int64_t T, int64_t H, void* codes, uint8_t* scales, float* inv_rms,
                             int64_t withheld_tile, int64_t wait_limit_ns, void* stream);
 
+/* The drill of the weight gradient: mxnorm_linear_wgrad_ckpt with one load of
+ * its pipeline never issued, load 0 (dout) or 1 (the codes) of stage
+ * withheld_stage (64 rows each, counted from 0 over the stages of each CTA
+ * pair's work; one past the last withholds nothing), and with waits of
+ * wait_limit_ns, 1e6 to 1e9, instead of 2 s.  The waits behind the load run
+ * out, bit 4 of mxnorm_device_errors is set, dw is invalid, and the call
+ * returns within a few limits with the context usable. */
+int mxnorm_linear_wgrad_wait_drill(const void* x_codes, const uint8_t* x_scales, int scale_layout,
+                                   const float* inv_rms, const void* dout, int64_t T, int64_t K, int64_t N, void* dw,
+                                   void* workspace, int64_t workspace_bytes, int withheld_load, int64_t withheld_stage,
+                                   int64_t wait_limit_ns, void* stream);
+
 /* Device-side error word of the current device, or'ed by kernels whose
  * bounded waits gave up (bit 0: a shared-memory pipeline wait of the tiled
  * variant timed out; bit 1: one of mxnorm_linear_fwd; bit 2: the device

@@ -22,6 +22,7 @@ __all__ = [
     "code_bytes", "bwd_ste", "quant_fwd_nvfp4", "absmax", "nvfp4_tensor_scale", "quant_fwd_mma", "mx_cast",
     "linear_fwd", "mma_scale_bytes", "tiled_wait_drill", "mx_cast_fp4", "nvfp4_tensor_scale_gain",
     "quant_fwd_nvfp4_mma", "mx_dequant", "linear_fwd_fp4", "bwd_ste_ckpt", "linear_wgrad_ckpt",
+    "linear_wgrad_wait_drill",
 ]
 
 FMT = {"mxfp8": 0, "mxfp4": 1, "mxfp4_h16": 2, "mxfp8_h16": 3, "mxfp4_h32": 4, "mxfp8_h32": 5}
@@ -111,6 +112,8 @@ def lib() -> ctypes.CDLL:
     L.mxnorm_linear_wgrad_workspace_bytes.restype = i64
     L.mxnorm_linear_wgrad_ckpt.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, i64, vp]
     L.mxnorm_linear_wgrad_ckpt.restype = i32
+    L.mxnorm_linear_wgrad_wait_drill.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, i64, i32, i64, i64, vp]
+    L.mxnorm_linear_wgrad_wait_drill.restype = i32
     L.mxnorm_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
     L.mxnorm_device_errors.restype = i32
     _lib = L
@@ -684,6 +687,10 @@ def linear_wgrad_ckpt(x_codes, x_scales, inv_rms, dout, layout: str = "mma", out
     float32 [T] or None (ones); dout: contiguous bf16 CUDA tensor [T, N]
     (N % 8 == 0).  A split sum's workspace is allocated per call (torch's
     allocator, on the call's stream).  Returns dw (bf16 [N, K], overwritten)."""
+    return _wgrad("mxnorm_linear_wgrad_ckpt", x_codes, x_scales, inv_rms, dout, layout, out, stream)
+
+
+def _wgrad(entry, x_codes, x_scales, inv_rms, dout, layout, out, stream, *drill):
     import torch
     lay = _layout_of(layout)
     if getattr(x_codes, "dim", lambda: 0)() != 2 or getattr(dout, "dim", lambda: 0)() != 2:
@@ -706,9 +713,19 @@ def linear_wgrad_ckpt(x_codes, x_scales, inv_rms, dout, layout: str = "mma", out
         _need(dw, "out", index, N * K, torch.bfloat16)
     need = lib().mxnorm_linear_wgrad_workspace_bytes(T, K, N)
     ws = _empty((need,), torch.uint8, dev, stream) if need > 0 else None
-    _launch(lib().mxnorm_linear_wgrad_ckpt, dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), lay, _ptr(inv_rms),
-            dout.data_ptr(), T, K, N, dw.data_ptr(), _ptr(ws), max(0, need))
+    _launch(getattr(lib(), entry), dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), lay, _ptr(inv_rms),
+            dout.data_ptr(), T, K, N, dw.data_ptr(), _ptr(ws), max(0, need), *drill)
     return dw
+
+
+def linear_wgrad_wait_drill(x_codes, x_scales, inv_rms, dout, layout: str = "mma", withheld_load: int = 0,
+                            withheld_stage: int = 0, wait_limit_ns: int = 2_000_000, out=None, stream=None):
+    """Failure-detection drill (mxnorm_linear_wgrad_wait_drill): the weight
+    gradient with one load of its pipeline withheld (0: dout's, 1: the
+    codes', of the given stage), so that its bounded waits expire and bit 4
+    of device_errors is set.  Returns dw, whose values are invalid."""
+    return _wgrad("mxnorm_linear_wgrad_wait_drill", x_codes, x_scales, inv_rms, dout, layout, out, stream,
+                  int(withheld_load), int(withheld_stage), int(wait_limit_ns))
 
 
 def tiled_wait_drill(x, withheld_tile: int = 0, wait_limit_ns: int = 2_000_000, out=None, stream=None):

@@ -160,6 +160,57 @@ int nvfp4_dev(const void* x, int64_t T, int64_t H, int p, const float* tensor_sc
   return MXNORM_OK;
 }
 
+// Drill arguments: a load (0 or 1) of a stage that is never issued, and the
+// waits' limit, 1 ms to 1 s: long beside any copy, so that a wait that ran out
+// also shows that the copies issued before it have landed.
+int check_drill(int64_t T, int load, int64_t stage, int64_t limit_ns, WaitDrill* drill) {
+  if (T == 0) return fail(MXNORM_ERR_INVALID_ARG, "the drill needs at least one row");
+  if (load != 0 && load != 1) return fail(MXNORM_ERR_INVALID_ARG, "withheld_load = %d is not 0 or 1", load);
+  if (stage < 0) return fail(MXNORM_ERR_INVALID_ARG, "withheld_stage = %lld < 0", (long long)stage);
+  if (limit_ns < 1000000 || limit_ns > 1000000000)
+    return fail(MXNORM_ERR_INVALID_ARG, "wait_limit_ns = %lld is not in [1e6, 1e9]", (long long)limit_ns);
+  drill->limit_ns = (unsigned long long)limit_ns;
+  drill->stage = stage;
+  drill->load = load;
+  return MXNORM_OK;
+}
+
+int wgrad(const void* x_codes, const uint8_t* x_scales, int scale_layout, const float* inv_rms, const void* dout,
+          int64_t T, int64_t K, int64_t N, void* dw, void* workspace, int64_t workspace_bytes, const WaitDrill& drill,
+          void* stream) {
+  int st = check_quantised("T", T, "K", K, MXNORM_FMT_MXFP8_E4M3, scale_layout);
+  if (st != MXNORM_OK) return st;
+  if (N <= 0 || N % 8 != 0)
+    return fail(MXNORM_ERR_INVALID_ARG, "N = %lld is not a positive multiple of 8", (long long)N);
+  if (T > (1 << 30) || N > (1 << 24))  // row coordinates of the tile loads are 32-bit
+    return fail(MXNORM_ERR_UNSUPPORTED, "T = %lld or N = %lld too large", (long long)T, (long long)N);
+  if (!dw) return fail(MXNORM_ERR_INVALID_ARG, "NULL dw");
+  if (!aligned(dw, 16)) return fail(MXNORM_ERR_MISALIGNED, "dw is not 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // an empty sum
+    cudaError_t err = cudaMemsetAsync(dw, 0, (size_t)N * (size_t)K * 2, s);
+    if (err != cudaSuccess) return cuda_fail(err, "mxnorm_linear_wgrad_ckpt: zeroing dw");
+    return MXNORM_OK;
+  }
+  if (!x_codes || !x_scales || !dout) return fail(MXNORM_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned(x_codes, 16) || !aligned(dout, 16))
+    return fail(MXNORM_ERR_MISALIGNED, "x_codes and dout must be 16-byte aligned");
+  if (!aligned(inv_rms, 4)) return fail(MXNORM_ERR_MISALIGNED, "inv_rms is not 4-byte aligned");
+  const int64_t need = wgrad_workspace_bytes(T, K, N);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(MXNORM_ERR_INVALID_ARG, "the workspace holds %lld bytes, the call needs %lld",
+                  (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    if (!aligned(workspace, 16)) return fail(MXNORM_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+  }
+  cudaError_t err = launch_mxnorm_wgrad(
+      WgradArgs{x_codes, x_scales, scale_layout == MXNORM_SCALE_MMA, inv_rms, dout, T, K, N, dw, workspace,
+                drill},
+      s);
+  if (err != cudaSuccess) return cuda_fail(err, "mxnorm_linear_wgrad_ckpt launch");
+  return MXNORM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -515,35 +566,19 @@ int mxnorm_linear_wgrad_ckpt(const void* x_codes, const uint8_t* x_scales, int s
                              const void* dout, int64_t T, int64_t K, int64_t N, void* dw, void* workspace,
                              int64_t workspace_bytes, void* stream) {
   g_last_error.clear();
-  int st = check_quantised("T", T, "K", K, MXNORM_FMT_MXFP8_E4M3, scale_layout);
+  return wgrad(x_codes, x_scales, scale_layout, inv_rms, dout, T, K, N, dw, workspace, workspace_bytes, WaitDrill{},
+               stream);
+}
+
+int mxnorm_linear_wgrad_wait_drill(const void* x_codes, const uint8_t* x_scales, int scale_layout,
+                                   const float* inv_rms, const void* dout, int64_t T, int64_t K, int64_t N, void* dw,
+                                   void* workspace, int64_t workspace_bytes, int withheld_load, int64_t withheld_stage,
+                                   int64_t wait_limit_ns, void* stream) {
+  g_last_error.clear();
+  WaitDrill drill;
+  int st = check_drill(T, withheld_load, withheld_stage, wait_limit_ns, &drill);
   if (st != MXNORM_OK) return st;
-  if (N <= 0 || N % 8 != 0)
-    return fail(MXNORM_ERR_INVALID_ARG, "N = %lld is not a positive multiple of 8", (long long)N);
-  if (T > (1 << 30) || N > (1 << 24))  // row coordinates of the tile loads are 32-bit
-    return fail(MXNORM_ERR_UNSUPPORTED, "T = %lld or N = %lld too large", (long long)T, (long long)N);
-  if (!dw) return fail(MXNORM_ERR_INVALID_ARG, "NULL dw");
-  if (!aligned(dw, 16)) return fail(MXNORM_ERR_MISALIGNED, "dw is not 16-byte aligned");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T == 0) {  // an empty sum
-    cudaError_t err = cudaMemsetAsync(dw, 0, (size_t)N * (size_t)K * 2, s);
-    if (err != cudaSuccess) return cuda_fail(err, "mxnorm_linear_wgrad_ckpt: zeroing dw");
-    return MXNORM_OK;
-  }
-  if (!x_codes || !x_scales || !dout) return fail(MXNORM_ERR_INVALID_ARG, "NULL pointer argument");
-  if (!aligned(x_codes, 16) || !aligned(dout, 16))
-    return fail(MXNORM_ERR_MISALIGNED, "x_codes and dout must be 16-byte aligned");
-  if (!aligned(inv_rms, 4)) return fail(MXNORM_ERR_MISALIGNED, "inv_rms is not 4-byte aligned");
-  const int64_t need = wgrad_workspace_bytes(T, K, N);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need)
-      return fail(MXNORM_ERR_INVALID_ARG, "the workspace holds %lld bytes, the call needs %lld",
-                  (long long)(workspace ? workspace_bytes : 0), (long long)need);
-    if (!aligned(workspace, 16)) return fail(MXNORM_ERR_MISALIGNED, "workspace is not 16-byte aligned");
-  }
-  cudaError_t err = launch_mxnorm_wgrad(
-      WgradArgs{x_codes, x_scales, scale_layout == MXNORM_SCALE_MMA, inv_rms, dout, T, K, N, dw, workspace}, s);
-  if (err != cudaSuccess) return cuda_fail(err, "mxnorm_linear_wgrad_ckpt launch");
-  return MXNORM_OK;
+  return wgrad(x_codes, x_scales, scale_layout, inv_rms, dout, T, K, N, dw, workspace, workspace_bytes, drill, stream);
 }
 
 const char* mxnorm_status_string(int status) {

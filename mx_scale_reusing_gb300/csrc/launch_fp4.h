@@ -58,6 +58,14 @@ struct BwdCkptArgs {
   void* dx;                  // bf16 [T, H]
 };
 
+// Failure-detection drill of a kernel with a load pipeline: the waits' limit,
+// and one load that is never issued, so that the waits behind it run out.
+struct WaitDrill {
+  unsigned long long limit_ns = 2000000000ull;
+  int64_t stage = -1;  // of each CTA's (or pair's) stages, from 0; -1: none is withheld
+  int load = 0;        // which of the stage's loads
+};
+
 struct WgradArgs {
   const void* codes;         // E4M3 [T, K]
   const uint8_t* scales;     // E8M0
@@ -69,6 +77,7 @@ struct WgradArgs {
   int64_t N;
   void* dw;                  // bf16 [N, K]
   void* workspace;           // wgrad_workspace_bytes(T, K, N) bytes
+  WaitDrill drill = {};      // load 0: dout's tile, 1: the codes'
 };
 
 // launch_nvfp4 with the scales in the MMA atom layout where scale_tiled != 0.

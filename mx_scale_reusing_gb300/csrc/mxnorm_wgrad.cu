@@ -34,7 +34,10 @@
 // Where tiles are few, the rows are split over S pairs a tile: fp32 partial
 // sums go to the caller's workspace [S][N][K] and a second kernel adds them in
 // order (the same bits every time).  Rows past T load as zeros and get p = 0.
-// Waits are bounded (2 s); on expiry bit 0 of the error word is set.
+// Waits are bounded (2 s); on expiry bit 0 of the error word is set and the
+// waiter arrives on no barrier any more, so that no phase completes that the
+// copies or the MMAs have not earned: the other roles' waits run out in turn,
+// each lets its own copies and MMAs end, and TMEM is freed.
 #include <algorithm>
 
 #include "launch_fp4.h"
@@ -94,17 +97,14 @@ static_assert(turns_fit<Cfg<1, false>> && turns_fit<Cfg<2, false>> && turns_fit<
 
 // A wait without a result: the probe first, and the bounded wait only where no
 // earlier one ran out.
-__device__ __forceinline__ void wait_or_walk(uint32_t bar, uint32_t parity, bool& dead) {
+__device__ __forceinline__ void wait_or_walk(uint32_t bar, uint32_t parity, unsigned long long limit_ns, bool& dead) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
-  if (!ok && !dead) dead = !tc::wait_bounded(bar, parity, &g_wgrad_error_word);
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return tc::wait_warp(bar, parity, &g_wgrad_error_word);
+  if (!ok && !dead) dead = !tc::wait_bounded(bar, parity, &g_wgrad_error_word, limit_ns);
 }
 
 // MN-major operand with 128-byte swizzle: 64 columns x 8 rows an atom (1024
@@ -186,7 +186,8 @@ template <int MT, bool NARROW, bool V8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_c,
                  const uint8_t* __restrict__ scales, int tiled, const float* __restrict__ inv_rms,
-                 uint16_t* __restrict__ dw, float* __restrict__ ws, int64_t T, int K, int N, Plan plan) {
+                 uint16_t* __restrict__ dw, float* __restrict__ ws, int64_t T, int K, int N, Plan plan,
+                 WaitDrill drill) {
   using C = Cfg<MT, NARROW>;
   constexpr int F = MT * kFeat, kRingB = C::kRingB, kRingC = C::kRingC, kMaxG = C::kMaxG;
   constexpr int kStageB = C::kStageB, kStageC = C::kStageC, kStageP = C::kStageP;
@@ -213,6 +214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int num_k = (K + W - 1) / W;
   const int stages = (int)((T + kBT - 1) / kBT);
   const int64_t items = num_n * num_k * split;
+  auto wait_warp = [&drill](uint32_t bar, uint32_t parity) {
+    return tc::wait_warp(bar, parity, &g_wgrad_error_word, drill.limit_ns);
+  };
 
   if (threadIdx.x == 0) {
     auto init = [](uint32_t bar, uint32_t n, int count) {
@@ -247,12 +251,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     Ring<kRingB> q;
     bool ok = true;
+    int64_t left = drill.load == 0 ? drill.stage : -1;  // stages before the withheld one
     for (int64_t i = pair; i < items && ok; i += npairs) {
       const Item m = item_of(i, num_n, num_k, F, W, split, stages);
       const int nx = m.n0 + 128 * (int)rank;
       for (int st = m.st0; st < m.st1; ++st, q.next()) {
         if (!q.first && !(ok = wait_warp(ab_empty0 + 8 * q.s, q.phase ^ 1u))) break;
-        if (elect_one()) {
+        if (left-- != 0 && elect_one()) {
           if (rank == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(ab_full0 + 8 * q.s),
                          "r"(2 * MT * kStageA)
@@ -267,11 +272,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    // every copy issued (both CTAs') has landed before the pair may exit
+    // every copy issued (both CTAs') has landed before the pair may exit; once a wait has run out, the last copy was
+    // issued a whole limit ago
     uint32_t ph;
     if (rank == 0)
       for (int j = 0; j < kRingB; ++j)
-        if (q.last(j, ph)) (void)wait_warp(ab_full0 + 8 * j, ph);
+        if (q.last(j, ph) && !wait_warp(ab_full0 + 8 * j, ph)) break;
   } else if (warp == 1) {
     if (rank == 0) {
       // One wait, 4 MT MMAs and one commit a stage, the descriptors by addition: this warp's own time can bound the
@@ -321,12 +327,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     Ring<kRingC> q;
     bool ok = true;
+    int64_t left = drill.load == 1 ? drill.stage : -1;
     for (int64_t i = pair; i < items && ok; i += npairs) {
       const Item m = item_of(i, num_n, num_k, F, W, split, stages);
       const int kx = m.k0 + HW * (int)rank;
       for (int st = m.st0; st < m.st1; ++st, q.next()) {
         if (!q.first && !(ok = wait_warp(c_empty0 + 8 * q.s, q.phase ^ 1u))) break;
-        if (elect_one()) {
+        if (left-- != 0 && elect_one()) {
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(c_full0 + 8 * q.s), "r"(kStageC)
                        : "memory");
           tma_2d(saddr(sC + q.s * kStageC), &tm_c, kx, st * kBT, c_full0 + 8 * q.s);
@@ -336,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     uint32_t ph;
     for (int j = 0; j < kRingC; ++j)
-      if (q.last(j, ph)) (void)wait_warp(c_full0 + 8 * j, ph);
+      if (q.last(j, ph) && !wait_warp(c_full0 + 8 * j, ph)) break;
   } else if (warp < kFirstEpi) {
     // 2^e of the G blocks of this CTA's columns, and rho~ of the rows.  Neighbouring lanes take neighbouring blocks of
     // a row, so that a load instruction touches 32 / G rows' sectors and not 32.
@@ -449,15 +456,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Ring<kRingB> rb;
     Ring<kRingC> rc;
     int turn = 0;
-    // A lane whose wait ran out waits no more but walks on, so that every lane takes part in every barrier (a vote a
-    // wait, to stop the warp as one, cost 10 % at 2043 x 768 x 768).
+    // A lane whose wait ran out waits no more but walks on, so that every lane takes part in every warp barrier (a vote
+    // a wait, to stop the warp as one, cost 10 % at 2043 x 768 x 768).  Lane 0 arrives for the warp, and once its own
+    // wait has run out it arrives no more: what the lanes then read and write is of no consequence.
     bool dead = false;
     for (int64_t i = pair; i < items; i += npairs) {
       const Item m = item_of(i, num_n, num_k, F, W, split, stages);
       for (int st = m.st0; st < m.st1; ++st, rb.next(), rc.next(), turn = (turn + 1) % kHGroups) {
         if (turn != group) continue;
-        wait_or_walk(c_full0 + 8 * rc.s, rc.phase, dead);
-        wait_or_walk(p_full0 + 8 * rc.s, rc.phase, dead);
+        wait_or_walk(c_full0 + 8 * rc.s, rc.phase, drill.limit_ns, dead);
+        wait_or_walk(p_full0 + 8 * rc.s, rc.phase, drill.limit_ns, dead);
         uint4 a, b;
         float pf = 0.0f;
         if (mine) {
@@ -468,8 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pf = __fmul_rn(ps[kBT * kMaxG + row], ps[row * G + blk]);
         }
         __syncwarp();
-        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(c_empty0 + 8 * rc.s) : "memory");
-        if (!rb.first) wait_or_walk(ab_empty0 + 8 * rb.s, rb.phase ^ 1u, dead);
+        if (lane == 0 && !dead)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(c_empty0 + 8 * rc.s) : "memory");
+        if (!rb.first) wait_or_walk(ab_empty0 + 8 * rb.s, rb.phase ^ 1u, drill.limit_ns, dead);
         if (mine) {
           const uint32_t dst = saddr(sB + rb.s * kStageB);
           const unsigned long long p = f2_pack(pf, pf);
@@ -489,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_remote(map_to_rank(ab_full0 + 8 * rb.s, 0));
+        if (lane == 0 && !dead) arrive_remote(map_to_rank(ab_full0 + 8 * rb.s, 0));
       }
     }
   }
@@ -558,7 +567,7 @@ cudaError_t launch_plan(const WgradArgs& a, const Plan& p, int grid, const CUten
   auto kern = (dst & 31) == 0 ? wgrad_kernel<MT, NARROW, true> : wgrad_kernel<MT, NARROW, false>;
   return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), Cfg<MT, NARROW>::kSmem, s, tm_d, tm_c, a.scales,
                     a.scale_tiled, a.inv_rms, static_cast<uint16_t*>(a.dw), static_cast<float*>(a.workspace), a.T,
-                    (int)a.K, (int)a.N, p);
+                    (int)a.K, (int)a.N, p, a.drill);
 }
 
 // CTA pairs that the current device runs at the same time, cached per device.

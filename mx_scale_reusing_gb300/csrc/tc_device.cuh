@@ -13,7 +13,7 @@
 namespace mxnorm {
 namespace tc {
 
-constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every mbarrier wait
+constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every mbarrier wait, drills apart
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -40,13 +40,14 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0u;
 }
 
-// Bounded wait (kWaitNs by %globaltimer); false (and bit 0 of *error set) on
+// Bounded wait (limit_ns by %globaltimer); false (and bit 0 of *error set) on
 // timeout.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, unsigned int* error) {
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, unsigned int* error,
+                                             unsigned long long limit_ns = kWaitNs) {
   if (try_wait(bar, parity)) return true;
   const unsigned long long t0 = gtimer();
   while (!try_wait(bar, parity)) {
-    if (gtimer() - t0 > kWaitNs) {
+    if (gtimer() - t0 > limit_ns) {
       atomicOr(error, 1u);
       return false;
     }
@@ -65,8 +66,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The wait of a whole warp: true in every lane, or false in every lane.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned int* error) {
-  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, error));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned int* error,
+                                          unsigned long long limit_ns = kWaitNs) {
+  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, error, limit_ns));
 }
 
 // A walk over a ring of DEPTH slots: slot and phase parity (a 64-bit stage
