@@ -298,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t accum = 0;
         for (int st = m.st0; st < m.st1; ++st, q.next()) {
           const uint64_t da = a0 + (uint64_t)((q.s * MT * kStageA) >> 4), db = b0 + (uint64_t)((q.s * kStageB) >> 4);
-          if (!(ok = wait_warp(ab_full0 + 8 * q.s, q.phase))) break;
+          if (!(ok = tc::wait_warp<true>(ab_full0 + 8 * q.s, q.phase, &g_wgrad_error_word, drill.limit_ns))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
 #pragma unroll
@@ -498,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0 && !dead) arrive_remote(map_to_rank(ab_full0 + 8 * rb.s, 0));
+        if (lane == 0 && !dead) arrive_remote_release(map_to_rank(ab_full0 + 8 * rb.s, 0));
       }
     }
   }

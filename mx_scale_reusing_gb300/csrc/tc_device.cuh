@@ -30,23 +30,35 @@ __device__ __forceinline__ unsigned long long gtimer() {
 // roles sleep too: letting them spin measured 11 % slower.
 constexpr uint32_t kSuspendHintNs = 1000000u;
 
+// CLUSTER: acquires what the peer CTA's threads wrote before an arrival with
+// cluster scope (arrive_remote_release).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
   return ok != 0u;
 }
 
 // Bounded wait (limit_ns by %globaltimer); false (and bit 0 of *error set) on
 // timeout.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, unsigned int* error,
                                              unsigned long long limit_ns = kWaitNs) {
-  if (try_wait(bar, parity)) return true;
+  if (try_wait<CLUSTER>(bar, parity)) return true;
   const unsigned long long t0 = gtimer();
-  while (!try_wait(bar, parity)) {
+  while (!try_wait<CLUSTER>(bar, parity)) {
     if (gtimer() - t0 > limit_ns) {
       atomicOr(error, 1u);
       return false;
@@ -66,9 +78,10 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The wait of a whole warp: true in every lane, or false in every lane.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned int* error,
                                           unsigned long long limit_ns = kWaitNs) {
-  return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, error, limit_ns));
+  return __all_sync(0xFFFFFFFFu, wait_bounded<CLUSTER>(bar, parity, error, limit_ns));
 }
 
 // A walk over a ring of DEPTH slots: slot and phase parity (a 64-bit stage
@@ -99,11 +112,21 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Arrive on an mbarrier of either CTA.  The default (CTA-scope) release:
-// what the waiter needs ordered is the tcgen05 work fenced around the
-// barrier, and a cluster-scope release here costs microseconds per arrival.
+// Arrive on an mbarrier of either CTA, once TMEM has been read.  The default
+// (CTA-scope) release: what the waiter needs ordered is the tcgen05 work
+// fenced around the barrier, and a cluster-scope release here, which waits for
+// the epilogue's global stores, costs microseconds per arrival.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Arrive on an mbarrier of either CTA, handing over what this warp wrote to
+// shared memory with ordinary stores (each lane's fence.proxy.async and a
+// __syncwarp before it, try_wait<true> at the other end).  The writes are made
+// in one CTA and read by MMAs that the other issues, so release and acquire
+// have cluster scope.
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // All threads of both CTAs (per-thread form: callers may arrive diverged).
