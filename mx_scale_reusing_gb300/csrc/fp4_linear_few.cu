@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t tx = (uint32_t)(kFeat * kStepBytes + R * kStepBytes + sf_bytes);
     int s = 0, filled = 0;
     uint32_t phase = 0;
+    bool ok = true;
     for (int kt = kt0; kt < kt1; ++kt) {
-      if (filled >= stages && !wait_warp(empty0 + 8 * s, phase ^ 1u)) break;
+      if (filled >= stages && !(ok = wait_warp(empty0 + 8 * s, phase ^ 1u))) break;
       if (elect_one()) {
         const uint32_t fb = full0 + 8 * s;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb), "r"(tx) : "memory");
@@ -243,8 +244,12 @@ __global__ void __launch_bounds__(kThreads)
         phase ^= 1u;
       }
     }
-    // every copy issued has landed before the CTA may exit
-    for (int j = 0; j < min(stages, filled); ++j) (void)wait_warp(full0 + 8 * j, j < s ? phase : phase ^ 1u);
+    // every copy issued has landed and every commit has arrived before the CTA may exit: the last commit of each slot
+    // shows both; once a wait has run out, the copies alone (the last one was then issued a whole limit ago)
+    for (int j = 0; j < min(stages, filled) && ok; ++j) ok = wait_warp(empty0 + 8 * j, j < s ? phase : phase ^ 1u);
+    if (!ok)
+      for (int j = 0; j < min(stages, filled); ++j)
+        if (!wait_warp(full0 + 8 * j, j < s ? phase : phase ^ 1u)) break;
   } else if (warp == 1) {
     const int last_mmas = (K - (num_kt - 1) * kStepElems + 63) / 64;
     const uint64_t a0 = desc_sw128(saddr(sA)), b0 = desc_sw128(saddr(sB)), f0 = desc_atom(saddr(sSF));

@@ -206,11 +206,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // every copy issued (both CTAs') must have landed before the pair may
-      // exit: the leader waits for its barriers' last phases
-      if (rank == 0)
-        for (int64_t i = (it > kStages ? it - kStages : 0); i < it; ++i)
-          (void)wait_bounded(full0 + 8 * (int)(i % kStages), (uint32_t)(i / kStages) & 1u);
+      // Neither CTA may exit before the commits that arrive here have, nor
+      // the pair before its copies have landed: the last commit of each slot
+      // shows both.  Once a wait has run out, the pair's copies alone; the
+      // last one was then issued a whole limit ago.
+      const int64_t first = it > kStages ? it - kStages : 0;
+      for (int64_t i = first; i < it && ok; ++i)
+        ok = wait_bounded(empty0 + 8 * (int)(i % kStages), (uint32_t)(i / kStages) & 1u);
+      if (!ok && rank == 0)
+        for (int64_t i = first; i < it; ++i)
+          if (!wait_bounded(full0 + 8 * (int)(i % kStages), (uint32_t)(i / kStages) & 1u)) break;
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {

@@ -272,10 +272,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    // every copy issued (both CTAs') has landed before the pair may exit; once a wait has run out, the last copy was
-    // issued a whole limit ago
+    // Neither CTA may exit before the commits that arrive here have, nor the pair before its copies have landed: the
+    // last commit of each slot shows both.  Once a wait has run out, the pair's copies alone; the last one was then
+    // issued a whole limit ago.
     uint32_t ph;
-    if (rank == 0)
+    for (int j = 0; j < kRingB && ok; ++j)
+      if (q.last(j, ph)) ok = wait_warp(ab_empty0 + 8 * j, ph);
+    if (!ok && rank == 0)
       for (int j = 0; j < kRingB; ++j)
         if (q.last(j, ph) && !wait_warp(ab_full0 + 8 * j, ph)) break;
   } else if (warp == 1) {
