@@ -77,8 +77,9 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<true>() <= 232448, "shared memory of a CTA");
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return tc::wait_warp(bar, parity, &g_fp4_linear_error_word);
+  return tc::wait_warp<CLUSTER>(bar, parity, &g_fp4_linear_error_word);
 }
 
 template <bool NV>
@@ -264,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int64_t i = pair; i < items && ok; i += npairs, ++tcount) {
         const int n = i < whole ? BN : BN / 2;
-        if (tcount > 0 && !(ok = wait_warp(acc_empty, (uint32_t)((tcount - 1) & 1)))) break;
+        if (tcount > 0 && !(ok = wait_warp<true>(acc_empty, (uint32_t)((tcount - 1) & 1)))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int kt = 0; kt < num_kt; ++kt, q.next()) {
           if (!(ok = wait_warp(sf_full0 + 8 * q.s, q.phase))) break;

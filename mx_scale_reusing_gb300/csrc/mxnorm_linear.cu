@@ -112,8 +112,9 @@ __device__ __forceinline__ uint32_t idesc_mxf8(int sf) {
          ((uint32_t)sf << 29);
 }
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
-  return tc::wait_bounded(bar, parity, &g_linear_error_word);
+  return tc::wait_bounded<CLUSTER>(bar, parity, &g_linear_error_word);
 }
 
 template <bool kV8>
@@ -222,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int64_t it = 0, tcount = 0;
       bool ok = true;
       for (int64_t tile = pair; tile < tiles && ok; tile += npairs, ++tcount) {
-        if (tcount > 0 && !(ok = wait_bounded(acc_empty, (uint32_t)((tcount - 1) & 1)))) break;
+        if (tcount > 0 && !(ok = wait_bounded<true>(acc_empty, (uint32_t)((tcount - 1) & 1)))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int kt = 0; kt < num_kt; ++kt, ++it) {
           const int s = (int)(it % kStages);

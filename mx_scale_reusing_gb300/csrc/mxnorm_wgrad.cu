@@ -217,6 +217,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto wait_warp = [&drill](uint32_t bar, uint32_t parity) {
     return tc::wait_warp(bar, parity, &g_wgrad_error_word, drill.limit_ns);
   };
+  auto wait_pair = [&drill](uint32_t bar, uint32_t parity) {  // for arrivals of both CTAs
+    return tc::wait_warp<true>(bar, parity, &g_wgrad_error_word, drill.limit_ns);
+  };
 
   if (threadIdx.x == 0) {
     auto init = [](uint32_t bar, uint32_t n, int count) {
@@ -295,13 +298,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // one accumulator: the two halves of TMEM in turn; two: both, once the tile before is read
         const int b = MT == 1 ? (int)(tcount & 1) : 0;
         const int64_t use = MT == 1 ? tcount / 2 : tcount;
-        if (use > 0 && !(ok = wait_warp(acc_empty0 + 8 * b, (uint32_t)(use - 1) & 1u))) break;
+        if (use > 0 && !(ok = wait_pair(acc_empty0 + 8 * b, (uint32_t)(use - 1) & 1u))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t acc = tmem + 256 * b;
         uint32_t accum = 0;
         for (int st = m.st0; st < m.st1; ++st, q.next()) {
           const uint64_t da = a0 + (uint64_t)((q.s * MT * kStageA) >> 4), db = b0 + (uint64_t)((q.s * kStageB) >> 4);
-          if (!(ok = tc::wait_warp<true>(ab_full0 + 8 * q.s, q.phase, &g_wgrad_error_word, drill.limit_ns))) break;
+          if (!(ok = wait_pair(ab_full0 + 8 * q.s, q.phase))) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
 #pragma unroll

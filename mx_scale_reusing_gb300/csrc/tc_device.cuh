@@ -30,8 +30,8 @@ __device__ __forceinline__ unsigned long long gtimer() {
 // roles sleep too: letting them spin measured 11 % slower.
 constexpr uint32_t kSuspendHintNs = 1000000u;
 
-// CLUSTER: acquires what the peer CTA's threads wrote before an arrival with
-// cluster scope (arrive_remote_release).
+// CLUSTER: for arrivals of the peer CTA's threads (arrive_remote and
+// arrive_remote_release).
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -112,12 +112,14 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Arrive on an mbarrier of either CTA, once TMEM has been read.  The default
-// (CTA-scope) release: what the waiter needs ordered is the tcgen05 work
-// fenced around the barrier, and a cluster-scope release here, which waits for
-// the epilogue's global stores, costs microseconds per arrival.
+// Arrive on an mbarrier of either CTA, once TMEM has been read: the
+// accumulators' hand-back, after tcgen05.wait::ld, tcgen05.fence::before_thread_sync
+// and a __syncwarp.  All that the waiter's MMAs need ordered is that tcgen05
+// work, which the fences at both ends order, so the arrival itself is relaxed
+// (at cluster scope: the waiter may be in the other CTA).  A release here,
+// which waits for the epilogue's global stores, costs microseconds per arrival.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Arrive on an mbarrier of either CTA, handing over what this warp wrote to
