@@ -442,6 +442,17 @@ int mxnorm_abi_version(void);
 int mxnorm_tiled_wait_drill(const void* x, int64_t T, int64_t H, void* codes, uint8_t* scales, float* inv_rms,
                             int64_t withheld_tile, int64_t wait_limit_ns, void* stream);
 
+/* The drill of the FP4 product: mxnorm_linear_fp4_fwd with the loads of stage
+ * withheld_stage never issued (256 elements of K a stage, counted from 0 over
+ * each CTA's or CTA pair's work; one past the last withholds nothing), and
+ * with waits of wait_limit_ns, 1e6 to 1e9, instead of 2 s.  The waits behind
+ * the loads run out, bit 3 of mxnorm_device_errors is set, out is invalid, and
+ * the call returns within a few limits with the context usable. */
+int mxnorm_linear_fp4_wait_drill(const void* x_codes, const uint8_t* x_scales, const float* inv_rms,
+                                 const void* w_codes, const uint8_t* w_scales, int64_t T, int64_t K, int64_t N, int fmt,
+                                 const float* x_tensor_scale, const float* w_tensor_scale, void* out,
+                                 int64_t withheld_stage, int64_t wait_limit_ns, void* stream);
+
 /* The drill of the weight gradient: mxnorm_linear_wgrad_ckpt with one load of
  * its pipeline never issued, load 0 (dout) or 1 (the codes) of stage
  * withheld_stage (64 rows each, counted from 0 over the stages of each CTA

@@ -22,7 +22,7 @@ __all__ = [
     "code_bytes", "bwd_ste", "quant_fwd_nvfp4", "absmax", "nvfp4_tensor_scale", "quant_fwd_mma", "mx_cast",
     "linear_fwd", "mma_scale_bytes", "tiled_wait_drill", "mx_cast_fp4", "nvfp4_tensor_scale_gain",
     "quant_fwd_nvfp4_mma", "mx_dequant", "linear_fwd_fp4", "bwd_ste_ckpt", "linear_wgrad_ckpt",
-    "linear_wgrad_wait_drill",
+    "linear_fp4_wait_drill", "linear_wgrad_wait_drill",
 ]
 
 FMT = {"mxfp8": 0, "mxfp4": 1, "mxfp4_h16": 2, "mxfp8_h16": 3, "mxfp4_h32": 4, "mxfp8_h32": 5}
@@ -106,6 +106,8 @@ def lib() -> ctypes.CDLL:
     L.mx_dequant_fwd.restype = i32
     L.mxnorm_linear_fp4_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, vp, vp]
     L.mxnorm_linear_fp4_fwd.restype = i32
+    L.mxnorm_linear_fp4_wait_drill.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, vp, i64, i64, vp]
+    L.mxnorm_linear_fp4_wait_drill.restype = i32
     L.mxnorm_bwd_ste_ckpt.argtypes = [vp, vp, i32, vp, vp, i64, i64, vp, vp]
     L.mxnorm_bwd_ste_ckpt.restype = i32
     L.mxnorm_linear_wgrad_workspace_bytes.argtypes = [i64, i64, i64]
@@ -618,6 +620,12 @@ def linear_fwd_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt: str = "mx
     x_codes uint8 [T, K/2] (any T from a single token), w_codes uint8
     [N, K/2]; inv_rms float32 [T] or None (ones); the tensor scales are for
     "nvfp4".  Returns out [T, N] (bf16)."""
+    return _linear_fp4("mxnorm_linear_fp4_fwd", x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_tensor_scale,
+                       w_tensor_scale, out, stream)
+
+
+def _linear_fp4(entry, x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_tensor_scale, w_tensor_scale, out, stream,
+                *drill):
     import torch
     f = _fmt_of(FP4_FMT, fmt)
     if getattr(x_codes, "dim", lambda: 0)() != 2 or getattr(w_codes, "dim", lambda: 0)() != 2:
@@ -642,10 +650,20 @@ def linear_fwd_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt: str = "mx
         out = _empty((T, N), torch.bfloat16, dev, stream)
     else:
         _need(out, "out", index, T * N, torch.bfloat16)
-    _launch(lib().mxnorm_linear_fp4_fwd, dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), _ptr(inv_rms),
+    _launch(getattr(lib(), entry), dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), _ptr(inv_rms),
             w_codes.data_ptr(), w_scales.data_ptr(), T, K, N, f, _ptr(x_tensor_scale), _ptr(w_tensor_scale),
-            out.data_ptr())
+            out.data_ptr(), *drill)
     return out
+
+
+def linear_fp4_wait_drill(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt: str = "mxfp4", x_tensor_scale=None,
+                          w_tensor_scale=None, withheld_stage: int = 0, wait_limit_ns: int = 2_000_000, out=None,
+                          stream=None):
+    """Failure-detection drill (mxnorm_linear_fp4_wait_drill): the FP4 product
+    with the loads of one stage withheld, so that its bounded waits expire
+    and bit 3 of device_errors is set.  Returns out, whose values are invalid."""
+    return _linear_fp4("mxnorm_linear_fp4_wait_drill", x_codes, x_scales, inv_rms, w_codes, w_scales, fmt,
+                       x_tensor_scale, w_tensor_scale, out, stream, int(withheld_stage), int(wait_limit_ns))
 
 
 # -------------------------------------------------------- 8-bit checkpoints

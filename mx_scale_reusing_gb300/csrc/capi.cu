@@ -175,6 +175,33 @@ int check_drill(int64_t T, int load, int64_t stage, int64_t limit_ns, WaitDrill*
   return MXNORM_OK;
 }
 
+int linear_fp4(const void* x_codes, const uint8_t* x_scales, const float* inv_rms, const void* w_codes,
+               const uint8_t* w_scales, int64_t T, int64_t K, int64_t N, int fmt, const float* x_tensor_scale,
+               const float* w_tensor_scale, void* out, const WaitDrill& drill, void* stream) {
+  if (!known_fmt(fmt)) return fail(MXNORM_ERR_INVALID_ARG, "unknown fmt %d", fmt);
+  if (!fp4_fmt(fmt))
+    return fail(MXNORM_ERR_UNSUPPORTED, "mxnorm_linear_fp4_fwd takes the FP4 formats only (fmt = %d)", fmt);
+  int st = check_quantised("T", T, "K", K, fmt, MXNORM_SCALE_MMA);
+  if (st != MXNORM_OK) return st;
+  if (N <= 0) return fail(MXNORM_ERR_INVALID_ARG, "N = %lld is not positive", (long long)N);
+  if (T > (1 << 30) || N > (1 << 24))  // row coordinates of the tile loads are 32-bit
+    return fail(MXNORM_ERR_UNSUPPORTED, "T = %lld or N = %lld too large", (long long)T, (long long)N);
+  if ((st = check_tensor_scale("x_tensor_scale", fmt, x_tensor_scale)) != MXNORM_OK) return st;
+  if ((st = check_tensor_scale("w_tensor_scale", fmt, w_tensor_scale)) != MXNORM_OK) return st;
+  if (T == 0) return MXNORM_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !out)
+    return fail(MXNORM_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(x_scales, 16) || !aligned(w_scales, 16) ||
+      !aligned(out, 16) || !aligned(inv_rms, 4))
+    return fail(MXNORM_ERR_MISALIGNED, "codes, scales and out need 16-byte alignment, inv_rms 4-byte");
+  cudaError_t err = launch_fp4_linear(Fp4LinearArgs{x_codes, x_scales, inv_rms, w_codes, w_scales, T, K, N,
+                                                    fmt == MXNORM_FMT_NVFP4, x_tensor_scale, w_tensor_scale, out,
+                                                    drill},
+                                      static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "mxnorm_linear_fp4_fwd launch");
+  return MXNORM_OK;
+}
+
 int wgrad(const void* x_codes, const uint8_t* x_scales, int scale_layout, const float* inv_rms, const void* dout,
           int64_t T, int64_t K, int64_t N, void* dw, void* workspace, int64_t workspace_bytes, const WaitDrill& drill,
           void* stream) {
@@ -517,27 +544,20 @@ int mxnorm_linear_fp4_fwd(const void* x_codes, const uint8_t* x_scales, const fl
                           const uint8_t* w_scales, int64_t T, int64_t K, int64_t N, int fmt,
                           const float* x_tensor_scale, const float* w_tensor_scale, void* out, void* stream) {
   g_last_error.clear();
-  if (!known_fmt(fmt)) return fail(MXNORM_ERR_INVALID_ARG, "unknown fmt %d", fmt);
-  if (!fp4_fmt(fmt))
-    return fail(MXNORM_ERR_UNSUPPORTED, "mxnorm_linear_fp4_fwd takes the FP4 formats only (fmt = %d)", fmt);
-  int st = check_quantised("T", T, "K", K, fmt, MXNORM_SCALE_MMA);
+  return linear_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, T, K, N, fmt, x_tensor_scale, w_tensor_scale, out,
+                    WaitDrill{}, stream);
+}
+
+int mxnorm_linear_fp4_wait_drill(const void* x_codes, const uint8_t* x_scales, const float* inv_rms,
+                                 const void* w_codes, const uint8_t* w_scales, int64_t T, int64_t K, int64_t N, int fmt,
+                                 const float* x_tensor_scale, const float* w_tensor_scale, void* out,
+                                 int64_t withheld_stage, int64_t wait_limit_ns, void* stream) {
+  g_last_error.clear();
+  WaitDrill drill;
+  int st = check_drill(T, 0, withheld_stage, wait_limit_ns, &drill);
   if (st != MXNORM_OK) return st;
-  if (N <= 0) return fail(MXNORM_ERR_INVALID_ARG, "N = %lld is not positive", (long long)N);
-  if (T > (1 << 30) || N > (1 << 24))  // row coordinates of the tile loads are 32-bit
-    return fail(MXNORM_ERR_UNSUPPORTED, "T = %lld or N = %lld too large", (long long)T, (long long)N);
-  if ((st = check_tensor_scale("x_tensor_scale", fmt, x_tensor_scale)) != MXNORM_OK) return st;
-  if ((st = check_tensor_scale("w_tensor_scale", fmt, w_tensor_scale)) != MXNORM_OK) return st;
-  if (T == 0) return MXNORM_OK;
-  if (!x_codes || !x_scales || !w_codes || !w_scales || !out)
-    return fail(MXNORM_ERR_INVALID_ARG, "NULL pointer argument");
-  if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(x_scales, 16) || !aligned(w_scales, 16) ||
-      !aligned(out, 16) || !aligned(inv_rms, 4))
-    return fail(MXNORM_ERR_MISALIGNED, "codes, scales and out need 16-byte alignment, inv_rms 4-byte");
-  cudaError_t err = launch_fp4_linear(Fp4LinearArgs{x_codes, x_scales, inv_rms, w_codes, w_scales, T, K, N,
-                                                    fmt == MXNORM_FMT_NVFP4, x_tensor_scale, w_tensor_scale, out},
-                                      static_cast<cudaStream_t>(stream));
-  if (err != cudaSuccess) return cuda_fail(err, "mxnorm_linear_fp4_fwd launch");
-  return MXNORM_OK;
+  return linear_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, T, K, N, fmt, x_tensor_scale, w_tensor_scale, out,
+                    drill, stream);
 }
 
 int mxnorm_bwd_ste_ckpt(const void* x_codes, const uint8_t* x_scales, int scale_layout, const void* dy,

@@ -77,11 +77,6 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<true>() <= 232448, "shared memory of a CTA");
 
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return tc::wait_warp<CLUSTER>(bar, parity, &g_fp4_linear_error_word);
-}
-
 template <bool NV>
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t accum) {
@@ -169,9 +164,10 @@ __device__ __forceinline__ Work work_of(int64_t i, int64_t whole, int64_t num_m,
 template <bool NV, int STORE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_wh, const __grid_constant__ CUtensorMap tm_sfx, const __grid_constant__ CUtensorMap tm_sfw,
+                      const __grid_constant__ CUtensorMap tm_wh, const __grid_constant__ CUtensorMap tm_sfx,
+                      const __grid_constant__ CUtensorMap tm_sfw,
                       const float* __restrict__ inv_rms, const float* __restrict__ xg, const float* __restrict__ wg,
-                      uint16_t* __restrict__ out, int64_t T, int K, int N, int64_t whole) {
+                      uint16_t* __restrict__ out, int64_t T, int K, int N, int64_t whole, WaitDrill drill) {
   using C = Cfg<NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -194,6 +190,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int last_mmas = (K - (num_kt - 1) * 2 * BK + 63) / 64;  // MMAs of the last stage
   const int64_t num_m = (T + 2 * BM - 1) / (2 * BM);
   const int64_t items = whole + 2 * (num_m * num_n - whole);
+  auto wait_warp = [&drill](uint32_t bar, uint32_t parity) {
+    return tc::wait_warp(bar, parity, &g_fp4_linear_error_word, drill.limit_ns);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -223,6 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     Ring<kStages> q;
     bool ok = true;
+    int64_t left = drill.stage;  // stages before the withheld one
     for (int64_t i = pair; i < items && ok; i += npairs) {
       const Work m = work_of(i, whole, num_m, num_n);
       const int xtile = (int)(2 * m.mt) + (int)rank;  // 128-row tile of x
@@ -230,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int bytes = m.full ? C::kStageBytes : C::kStageBytes - kStageB / 2 - C::kAtoms * 512;
       for (int kt = 0; kt < num_kt; ++kt, q.next()) {
         if (!q.first && !(ok = wait_warp(empty0 + 8 * q.s, q.phase ^ 1u))) break;
-        if (elect_one()) {
+        if (left-- != 0 && elect_one()) {
           const uint32_t fb = map_to_rank(full0 + 8 * q.s, 0);
           if (rank == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full0 + 8 * q.s),
@@ -265,7 +265,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int64_t i = pair; i < items && ok; i += npairs, ++tcount) {
         const int n = i < whole ? BN : BN / 2;
-        if (tcount > 0 && !(ok = wait_warp<true>(acc_empty, (uint32_t)((tcount - 1) & 1)))) break;
+        if (tcount > 0 &&
+            !(ok = tc::wait_warp<true>(acc_empty, (uint32_t)((tcount - 1) & 1), &g_fp4_linear_error_word,
+                                       drill.limit_ns)))
+          break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int kt = 0; kt < num_kt; ++kt, q.next()) {
           if (!(ok = wait_warp(sf_full0 + 8 * q.s, q.phase))) break;
@@ -417,7 +420,7 @@ cudaError_t launch_store(const Fp4LinearArgs& a, const CUtensorMap (&tm)[5], cud
   const int64_t whole = 2 * rest <= co_resident ? tiles - rest : tiles;
   const int grid = (int)(2 * std::min<int64_t>(whole + 2 * (tiles - whole), co_resident));
   return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem_bytes<NV>(), s, tm[0], tm[1], tm[2], tm[3], tm[4],
-                    a.inv_rms, a.xg, a.wg, static_cast<uint16_t*>(a.out), a.T, (int)a.K, (int)a.N, whole);
+                    a.inv_rms, a.xg, a.wg, static_cast<uint16_t*>(a.out), a.T, (int)a.K, (int)a.N, whole, a.drill);
 }
 
 template <bool NV>

@@ -41,10 +41,6 @@ constexpr int kSms = 152;
 constexpr size_t kSmemOne = 227 * 1024;  // one CTA per SM
 constexpr size_t kSmemTwo = 113 * 1024;  // two
 
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return tc::wait_warp(bar, parity, &g_fp4_few_error_word);
-}
-
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -171,7 +167,7 @@ __global__ void __launch_bounds__(kThreads)
                           const __grid_constant__ CUtensorMap tm_sfx, const __grid_constant__ CUtensorMap tm_sfw,
                           const float* __restrict__ inv_rms, const float* __restrict__ xg,
                           const float* __restrict__ wg, uint16_t* __restrict__ out, int64_t T, int K, int N, Few f,
-                          int l2_prefetch) {
+                          int l2_prefetch, WaitDrill drill) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int R = f.R, stages = f.stages;
@@ -192,6 +188,9 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t t0 = (int64_t)blockIdx.y * R;
   const int rows = (int)min((int64_t)R, T - t0);
   const int num_kt = (K + kStepElems - 1) / kStepElems;
+  auto wait_warp = [&drill](uint32_t bar, uint32_t parity) {
+    return tc::wait_warp(bar, parity, &g_fp4_few_error_word, drill.limit_ns);
+  };
   const int kt0 = (int)((int64_t)num_kt * rank / f.split), kt1 = (int)((int64_t)num_kt * (rank + 1) / f.split);
 
   if (threadIdx.x == 0) {
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     for (int kt = kt0; kt < kt1; ++kt) {
       if (filled >= stages && !(ok = wait_warp(empty0 + 8 * s, phase ^ 1u))) break;
-      if (elect_one()) {
+      if (kt - kt0 != drill.stage && elect_one()) {
         const uint32_t fb = full0 + 8 * s;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb), "r"(tx) : "memory");
         tma_2d(saddr(sA + s * kFeat * kStepBytes), &tm_w, kt * kStepBytes, n0, fb);
@@ -411,7 +410,7 @@ cudaError_t launch_few(const Fp4LinearArgs& a, cudaStream_t s) {
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], a.inv_rms, a.xg, a.wg,
                             static_cast<uint16_t*>(a.out), a.T, (int)a.K, (int)a.N, f,
-                            is_device_memory(a.w_codes) ? 1 : 0);
+                            is_device_memory(a.w_codes) ? 1 : 0, a.drill);
 }
 
 }  // namespace

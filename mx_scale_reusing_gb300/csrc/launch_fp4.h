@@ -32,6 +32,14 @@ struct DequantArgs {
   void* out;            // bf16 [T, H]
 };
 
+// Failure-detection drill of a kernel with a load pipeline: the waits' limit,
+// and one load that is never issued, so that the waits behind it run out.
+struct WaitDrill {
+  unsigned long long limit_ns = 2000000000ull;
+  int64_t stage = -1;  // of each CTA's (or pair's) stages, from 0; -1: none is withheld
+  int load = 0;        // which of the stage's loads
+};
+
 struct Fp4LinearArgs {
   const void* x_codes;       // E2M1 [T, K/2]
   const uint8_t* x_scales;   // MMA atoms
@@ -45,6 +53,7 @@ struct Fp4LinearArgs {
   const float* xg;           // NVFP4 tensor scales (device words)
   const float* wg;
   void* out;                 // bf16 [T, N]
+  WaitDrill drill = {};      // all loads of the stage
 };
 
 struct BwdCkptArgs {
@@ -56,14 +65,6 @@ struct BwdCkptArgs {
   int64_t T;
   int64_t H;
   void* dx;                  // bf16 [T, H]
-};
-
-// Failure-detection drill of a kernel with a load pipeline: the waits' limit,
-// and one load that is never issued, so that the waits behind it run out.
-struct WaitDrill {
-  unsigned long long limit_ns = 2000000000ull;
-  int64_t stage = -1;  // of each CTA's (or pair's) stages, from 0; -1: none is withheld
-  int load = 0;        // which of the stage's loads
 };
 
 struct WgradArgs {

@@ -30,3 +30,11 @@ def test_wgrad_drill_needs_the_workspace_of_the_call(L):
     f = L.mxnorm_linear_wgrad_wait_drill
     assert f(F, F, 0, F, F, 100000, 128, 64, F, F, n - 1, 0, 0, 2_000_000, None) == 1
     assert f(F, F, 0, F, F, 100000, 128, 64, F, F + 8, n, 0, 0, 2_000_000, None) == 3
+
+
+@pytest.mark.parametrize("bad", [dict(stage=-1), dict(ns=999_999), dict(ns=1_000_000_001), dict(T=0), dict(T=-1), dict(K=64),
+                                 dict(N=0), dict(fmt=9), dict(out=None), dict(xg=F)])
+def test_product_drill_refusals(L, bad):
+    a = dict(x=F, xs=F, inv=F, w=F, ws=F, T=8, K=128, N=64, fmt=1, xg=None, wg=None, out=F, stage=0, ns=2_000_000) | bad
+    assert L.mxnorm_linear_fp4_wait_drill(*a.values(), None) == 1
+    assert L.mxnorm_last_error()

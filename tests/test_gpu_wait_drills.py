@@ -69,3 +69,31 @@ def test_wgrad_drill_without_a_withheld_load_is_the_call():
     assert torch.equal(mx.linear_wgrad_ckpt(c, s, inv, dout, "row_major"),
                        mx.linear_wgrad_wait_drill(c, s, inv, dout, "row_major", 1, 1 << 40))
     assert mx.device_errors() == 0
+
+
+# few rows: K whole, split over two, four and eight CTAs, one and two CTAs an SM; many rows: one tile and several a
+# pair, halved tiles, rows of every alignment
+PRODUCT = [(3, 640, 1300), (1, 4096, 2048), (33, 4096, 2050), (65, 4096, 6144), (1, 1024, 28672), (128, 4096, 28672),
+           (300, 768, 1000), (700, 2304, 768), (2125, 4096, 2057), (2200, 384, 904)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("T,K,N", PRODUCT)
+def test_product_waits_expire_and_are_reported(T, K, N, fmt):
+    x, w = dev(synth.make_random_rows(T, K, 3, 2.0)), dev(synth.make_random_rows(64, K, 4, 0.05)).repeat(-(-N // 64), 1)[:N]
+    if fmt == "nvfp4":
+        xc, xs, inv, xg = mx.quant_fwd_nvfp4_mma(x)
+    else:
+        (xc, xs, inv), xg = mx.quant_fwd_mma(x, fmt=fmt), None
+    wc, ws, wg = mx.mx_cast_fp4(w.contiguous(), fmt)
+    args = (xc, xs, inv, wc, ws, fmt, xg, wg)
+    want = mx.linear_fwd_fp4(*args)
+    for stage in (0, 1, 7):
+        err, seconds = drilled(lambda o: mx.linear_fp4_wait_drill(*args, stage, out=o), T, N)
+        # work that has no such stage loses nothing; the first stage is everyone's
+        assert err in (0, 8) and (err == 8 or stage > 0)
+        assert seconds < 0.5, f"the drill took {seconds:.3f} s"
+        assert torch.equal(want, mx.linear_fwd_fp4(*args))
+        assert mx.device_errors() == 0
+    out = mx.linear_fp4_wait_drill(*args, 1 << 40)
+    assert torch.equal(want, out) and mx.device_errors() == 0
