@@ -305,6 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int st = m.st0; st < m.st1; ++st, q.next()) {
           const uint64_t da = a0 + (uint64_t)((q.s * MT * kStageA) >> 4), db = b0 + (uint64_t)((q.s * kStageB) >> 4);
           if (!(ok = wait_pair(ab_full0 + 8 * q.s, q.phase))) break;
+          acquire_shared_cluster();  // the peer's h
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
 #pragma unroll

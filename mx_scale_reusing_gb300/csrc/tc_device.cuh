@@ -30,14 +30,15 @@ __device__ __forceinline__ unsigned long long gtimer() {
 // roles sleep too: letting them spin measured 11 % slower.
 constexpr uint32_t kSuspendHintNs = 1000000u;
 
-// CLUSTER: for arrivals of the peer CTA's threads (arrive_remote and
-// arrive_remote_release).
+// CLUSTER: for arrivals of the peer CTA's threads.  Relaxed: the tcgen05
+// fences (arrive_remote) or acquire_shared_cluster (arrive_remote_release)
+// order what lies around it.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   if constexpr (CLUSTER)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
@@ -124,11 +125,18 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
 
 // Arrive on an mbarrier of either CTA, handing over what this warp wrote to
 // shared memory with ordinary stores (each lane's fence.proxy.async and a
-// __syncwarp before it, try_wait<true> at the other end).  The writes are made
-// in one CTA and read by MMAs that the other issues, so release and acquire
-// have cluster scope.
+// __syncwarp before it; at the other end try_wait<true>, then
+// acquire_shared_cluster).  The writes are made in one CTA and read by MMAs
+// that the other issues, so release and acquire have cluster scope; they are
+// restricted to shared memory, since a full release and acquire, which order
+// global memory too, took 0.4 us a stage (the weight gradient at 4096 x 2048 x
+// 2048: 54.6 us, 28.6 restricted).
 __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  arrive_remote(cluster_addr);
+}
+__device__ __forceinline__ void acquire_shared_cluster() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // All threads of both CTAs (per-thread form: callers may arrive diverged).
