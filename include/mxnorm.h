@@ -337,8 +337,9 @@ int mx_cast_fp4_fwd(const void* w, int64_t N, int64_t K, int fmt, const float* g
                     const float* tensor_scale, void* codes, uint8_t* scales, int scale_layout, void* stream);
 
 /* The NVFP4 tensor scale of the gain-folded weight: mxnorm_nvfp4_tensor_scale
- * over the values RN_fp32(w[n, k] g_k) (non-finite ones skipped).  w, gamma:
- * 16-byte aligned; K % 16 == 0.  N == 0 writes 1. */
+ * over the values RN_fp32(w[n, k] g_k) (non-finite ones skipped), and 1 where
+ * a / 2688 rounds to 0, which a gain makes possible.  w, gamma: 16-byte
+ * aligned; K % 16 == 0.  N == 0 writes 1. */
 int mxnorm_nvfp4_tensor_scale_gain(const void* w, int64_t N, int64_t K, const float* gamma, float c,
                                    float* tensor_scale, void* stream);
 

@@ -533,8 +533,8 @@ def _check_gain(w, gamma):
 
 def nvfp4_tensor_scale_gain(w, gamma=None, c: float = 1.0, stream=None):
     """The NVFP4 tensor scale of a gain-folded weight (the largest finite
-    |w[n, k] * RN_fp32(c * gamma[k])| / (448 * 6); 1 when there is none but
-    zero), derived on the device.  Returns a 1-element float32 CUDA tensor."""
+    |w[n, k] * RN_fp32(c * gamma[k])| / (448 * 6); 1 where that is 0 in
+    fp32), derived on the device.  Returns a 1-element float32 CUDA tensor."""
     import torch
     _check_gain(w, gamma)
     N, K = w.shape

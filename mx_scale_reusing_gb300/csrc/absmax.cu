@@ -1,6 +1,7 @@
 // absmax.cu -- the largest magnitude of a tensor or of a gain-folded weight,
 // and the NVFP4 tensor scale derived from it (RN(a / 2688), a the largest
-// finite magnitude; 1 where that is 0).
+// finite magnitude; 1 where that quotient is 0, for gain-folded values below
+// 2688 2^-150 too).
 //
 // Non-negative floats order like their bits, so a maximum is an integer
 // maximum of the magnitudes' bits (NaN above Inf above every finite value;
@@ -122,8 +123,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t m, uint32_t* red) {
 }
 
 __device__ __forceinline__ float scale_of(uint32_t bits) {
-  const float a = __uint_as_float(bits);
-  return a > 0.0f ? __fdiv_rn(a, 2688.0f) : 1.0f;
+  const float g = __fdiv_rn(__uint_as_float(bits), 2688.0f);
+  return g > 0.0f ? g : 1.0f;
 }
 
 // Starts as an ordinary launch, after everything before it on the stream; the
