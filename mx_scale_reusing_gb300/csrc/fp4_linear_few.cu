@@ -154,9 +154,16 @@ struct Few {
 };
 
 template <bool NV>
-__host__ __device__ inline int stage_bytes(int R) {
+__host__ __device__ constexpr int stage_bytes(int R) {
   return kFeat * kStepBytes + R * kStepBytes + 2 * kAtoms<NV> * 512;
 }
+// The partial sums of a split K, R x 128 floats, lie over the ring: they end
+// below the barriers since 4 R <= stages (128 + R) for R <= 128 and two stages,
+// which the smallest ring has.
+constexpr int extra_bytes(int R) { return 1024 + 8 * (2 * kMaxStages + 2) + 4 * R; }
+static_assert(((int)kSmemTwo - extra_bytes(kMaxRows)) / stage_bytes<true>(kMaxRows) >= 2 &&
+                  4 * kMaxRows <= 2 * (kFeat + kMaxRows),
+              "partial sums fit the ring");
 template <bool NV>
 constexpr int kSfCols = 8 * kAtoms<NV>;  // TMEM columns of a stage's scales, w then x
 __host__ __device__ inline int acc_cols(int R) { return R <= 32 ? 32 : (R + 31) & ~31; }
@@ -362,7 +369,7 @@ Few choose(int64_t T, int64_t K, int64_t N, size_t* smem) {
     if (f.R <= 32 ? tiles * s >= 2 * kSms : tiles * s > (s == 2 ? 256 : clusters_fit(s))) break;
     f.split = s;
   }
-  const int extra = 1024 + 8 * (2 * kMaxStages + 2) + 4 * f.R;
+  const int extra = extra_bytes(f.R);
   const int per = stage_bytes<NV>(f.R);
   // More CTAs than SMs share an SM two by two, with shallower rings, rather
   // than run in two waves (128 x 4096 x 28672: 20.7 us against 26.5).
@@ -372,7 +379,7 @@ Few choose(int64_t T, int64_t K, int64_t N, size_t* smem) {
   f.stages = std::min(f.stages, (tmem - acc_cols(f.R)) / kSfCols<NV>);
   f.tmem_cols = 32;
   while (f.tmem_cols < acc_cols(f.R) + f.stages * kSfCols<NV>) f.tmem_cols *= 2;
-  *smem = (size_t)std::max(f.stages * per, f.split > 1 ? f.R * kFeat * 4 : 0) + extra;
+  *smem = (size_t)(f.stages * per + extra);
   return f;
 }
 
