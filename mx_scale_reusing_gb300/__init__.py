@@ -508,6 +508,15 @@ def _need_scales(t, name, index, rows, H, fmt, layout):
     _need(t, name, index, _scale_bytes(rows, H, fmt, layout))
 
 
+def _need_inv_rms(t, index, rows):
+    """_need for the rows' factors, one a row, where they are given."""
+    import torch
+    if t is not None:
+        _need(t, "inv_rms", index, rows, torch.float32)
+        if t.numel() != rows:
+            raise ValueError(f"inv_rms holds {t.numel()} values for {rows} rows")
+
+
 def _fp4_out(rows, K, fmt, layout, device, out, stream):
     """(codes [rows, K/2], scales) for a cast: the caller's, checked, or new ones."""
     import torch
@@ -640,8 +649,7 @@ def _linear_fp4(entry, x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_ten
     _need(w_codes, "w_codes", index, 0)
     _need_scales(x_scales, "x_scales", index, T, K, fmt, "mma")
     _need_scales(w_scales, "w_scales", index, N, K, fmt, "mma")
-    if inv_rms is not None:
-        _need(inv_rms, "inv_rms", index, T, torch.float32)
+    _need_inv_rms(inv_rms, index, T)
     if x_tensor_scale is not None:
         _need(x_tensor_scale, "x_tensor_scale", index, 1, torch.float32)
     if w_tensor_scale is not None:
@@ -685,9 +693,9 @@ def bwd_ste_ckpt(x_codes, x_scales, dy, inv_rms, layout: str = "row_major", out=
     T = dy.numel() // H if H else 0
     _need(x_codes, "x_codes", index, 0)
     _need_scales(x_scales, "x_scales", index, T, H, "mxfp8", layout)
-    _need(inv_rms, "inv_rms", index, T, torch.float32)
-    if inv_rms.numel() != T:
-        raise ValueError("inv_rms needs one value per row")
+    if inv_rms is None:
+        raise ValueError("inv_rms must be a contiguous CUDA tensor")
+    _need_inv_rms(inv_rms, index, T)
     if out is None:
         dx = _empty(shape, torch.bfloat16, dev, stream)
     else:
@@ -722,8 +730,7 @@ def _wgrad(entry, x_codes, x_scales, inv_rms, dout, layout, out, stream, *drill)
     _need(x_codes, "x_codes", index, 0)
     _need_scales(x_scales, "x_scales", index, T, K, "mxfp8", layout)
     _need(dout, "dout", index, 0, torch.bfloat16)
-    if inv_rms is not None:
-        _need(inv_rms, "inv_rms", index, T, torch.float32)
+    _need_inv_rms(inv_rms, index, T)
     if out is None:
         dw = _empty((N, K), torch.bfloat16, dev, stream)
     else:

@@ -41,3 +41,22 @@ def test_no_value_but_zero_has_scale_one():
     w = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
     assert mx.nvfp4_tensor_scale_gain(w, torch.full((64,), 0.5, device="cuda")).item() == 1.0
     assert mx.nvfp4_tensor_scale(w).item() == 1.0
+
+
+@pytest.mark.parametrize("rows", [63, 65, 128])
+def test_inv_rms_of_other_rows_is_refused(rows):
+    """One factor a row: an inv_rms of a padded batch or of another one does not pass by its length."""
+    x = torch.randn((64, 256), device="cuda").to(torch.bfloat16)
+    w = torch.randn((136, 256), device="cuda").to(torch.bfloat16)
+    xc, xs, inv = mx.quant_fwd_mma(x, fmt="mxfp4")
+    wc, ws, _ = mx.mx_cast_fp4(w)
+    c, s, r = mx.quant_fwd(x)
+    other = torch.ones(rows, device="cuda")
+    dout = torch.randn((64, 136), device="cuda").to(torch.bfloat16)
+    for fn in (lambda f: mx.linear_fwd_fp4(xc, xs, f, wc, ws), lambda f: mx.linear_wgrad_ckpt(c, s, f, dout, "row_major"),
+               lambda f: mx.bwd_ste_ckpt(c, s, x, f)):
+        with pytest.raises(ValueError, match="inv_rms"):
+            fn(other)
+        fn(r)
+    with pytest.raises(ValueError, match="inv_rms"):
+        mx.bwd_ste_ckpt(c, s, x, None)
