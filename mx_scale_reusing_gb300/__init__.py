@@ -6,6 +6,11 @@ tensors, allocates outputs with torch and passes raw device pointers plus the
 current CUDA stream.  There is no CPU fallback: without the built library
 every call raises ``MXNormLibraryMissing``.
 
+A call runs on its `stream` argument, or on the device's current stream, and
+the caller orders its inputs there.  What the call allocates belongs to that
+stream's pool and, with `stream` given, is safe on the current stream as well;
+on a third stream it needs Tensor.record_stream as any tensor does.
+
 Method: "MXNorm: Reusing MXFP block scales for efficient tensor
 normalisation", Resumen tecnico, 2. Metodologia ("Fundamentos Teoricos":
 inverse RMS from the power mean of the MX block scales; "Implementacion":
@@ -162,14 +167,29 @@ def _device(device):
     return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _empty(shape, dtype, device, stream):
-    """An output or workspace from the memory pool of the stream that will
-    write it (`stream`, or the current one)."""
+def _workspace(shape, dtype, device, stream):
+    """Memory from the pool of the stream that will use it (`stream`, or the current one)."""
     import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # anything that names a cudaStream_t
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output from the pool of the stream that will write it.  With a
+    `stream` argument the current stream is recorded too: it usually reads
+    the output once it has waited for `stream`, and the memory is not used
+    again before both are done with it."""
+    import torch
+    t = _workspace(shape, dtype, device, stream)
+    if stream is not None:
+        current = torch.cuda.current_stream(device)
+        if current != stream:
+            t.record_stream(current)
+    return t
 
 
 def _launch(fn, device, stream, *args):
@@ -235,9 +255,9 @@ def quant_fwd(x, p: int = 2, fmt: str = "mxfp8", variant: str = "auto", out=None
     T = x.numel() // H if H else 0
     lead = tuple(x.shape[:-1])
     if out is None:
-        codes = torch.empty(lead + (code_bytes(H, fmt),), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(lead + (H // 32,), dtype=torch.uint8, device=x.device)
-        inv = torch.empty(lead, dtype=torch.float32, device=x.device)
+        codes = _empty(lead + (code_bytes(H, fmt),), torch.uint8, x.device, stream)
+        scales = _empty(lead + (H // 32,), torch.uint8, x.device, stream)
+        inv = _empty(lead, torch.float32, x.device, stream)
     else:
         codes, scales, inv = out
         _require(codes, "codes", x.device, min_numel=T * code_bytes(H, fmt), byte_elems=True)
@@ -260,10 +280,10 @@ def rmsnorm_mxfp8_ref_fwd(x, eps: float = 1e-5, out=None, stream=None):
     T = x.numel() // H if H else 0
     lead = tuple(x.shape[:-1])
     if out is None:
-        y = torch.empty_like(x)
-        codes = torch.empty(lead + (H,), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(lead + (H // 32,), dtype=torch.uint8, device=x.device)
-        inv = torch.empty(lead, dtype=torch.float32, device=x.device)
+        y = _empty(tuple(x.shape), torch.bfloat16, x.device, stream)
+        codes = _empty(lead + (H,), torch.uint8, x.device, stream)
+        scales = _empty(lead + (H // 32,), torch.uint8, x.device, stream)
+        inv = _empty(lead, torch.float32, x.device, stream)
     else:
         y, codes, scales, inv = out
         _require(y, "y", x.device, torch.bfloat16, T * H)
@@ -322,9 +342,9 @@ def quant_fwd_nvfp4(x, p: int = 2, tensor_scale=None, out=None, stream=None):
     if tensor_scale is None:
         tensor_scale = nvfp4_tensor_scale(x, stream)
     if out is None:
-        out = (torch.empty(lead + (H // 2,), dtype=torch.uint8, device=x.device),
-               torch.empty(lead + (H // 16,), dtype=torch.uint8, device=x.device),
-               torch.empty(lead, dtype=torch.float32, device=x.device))
+        out = (_empty(lead + (H // 2,), torch.uint8, x.device, stream),
+               _empty(lead + (H // 16,), torch.uint8, x.device, stream),
+               _empty(lead, torch.float32, x.device, stream))
     codes, scales, inv = out
     _require(codes, "codes", x.device, min_numel=T * (H // 2), byte_elems=True)
     _require(scales, "scales", x.device, min_numel=T * (H // 16), byte_elems=True)
@@ -352,11 +372,11 @@ def mma_scale_bytes(rows: int, H: int) -> int:
     return n
 
 
-def _scale_buffer(rows, H, layout, device):
+def _scale_buffer(rows, H, layout, device, stream):
     import torch
     if layout == "mma":
-        return torch.empty((mma_scale_bytes(rows, H),), dtype=torch.uint8, device=device)
-    return torch.empty((rows, H // 32), dtype=torch.uint8, device=device)
+        return _empty((mma_scale_bytes(rows, H),), torch.uint8, device, stream)
+    return _empty((rows, H // 32), torch.uint8, device, stream)
 
 
 def quant_fwd_mma(x, p: int = 2, fmt: str = "mxfp8", stream=None):
@@ -367,9 +387,9 @@ def quant_fwd_mma(x, p: int = 2, fmt: str = "mxfp8", stream=None):
         raise ValueError("x must be a contiguous bfloat16 CUDA tensor")
     H = x.shape[-1]
     T = x.numel() // H if H else 0
-    codes = torch.empty(tuple(x.shape[:-1]) + (code_bytes(H, fmt),), dtype=torch.uint8, device=x.device)
-    scales = _scale_buffer(T, H, "mma", x.device)
-    inv = torch.empty(tuple(x.shape[:-1]), dtype=torch.float32, device=x.device)
+    codes = _empty(tuple(x.shape[:-1]) + (code_bytes(H, fmt),), torch.uint8, x.device, stream)
+    scales = _scale_buffer(T, H, "mma", x.device, stream)
+    inv = _empty(tuple(x.shape[:-1]), torch.float32, x.device, stream)
     with _device(x.device):
         _check(lib().mxnorm_quant_fwd_layout(x.data_ptr(), T, H, int(p), FMT[fmt], codes.data_ptr(),
                                              scales.data_ptr(), inv.data_ptr(), 1, _stream_ptr(x.device, stream)))
@@ -383,8 +403,8 @@ def mx_cast(x, layout: str = "row_major", stream=None):
         raise ValueError("x must be a contiguous bfloat16 CUDA tensor")
     H = x.shape[-1]
     T = x.numel() // H if H else 0
-    codes = torch.empty(tuple(x.shape), dtype=torch.uint8, device=x.device)
-    scales = _scale_buffer(T, H, layout, x.device)
+    codes = _empty(tuple(x.shape), torch.uint8, x.device, stream)
+    scales = _scale_buffer(T, H, layout, x.device, stream)
     with _device(x.device):
         _check(lib().mx_cast_fwd(x.data_ptr(), T, H, 0, codes.data_ptr(), scales.data_ptr(), SCALE_LAYOUT[layout],
                                  _stream_ptr(x.device, stream)))
@@ -403,8 +423,8 @@ def mx_cast_gain(w, gamma, c: float = 1.0, layout: str = "mma", stream=None):
     _require(gamma, "gamma", w.device, torch.float32)
     if tuple(gamma.shape) != (K,):
         raise ValueError("gamma must hold K entries")
-    codes = torch.empty((N, K), dtype=torch.uint8, device=w.device)
-    scales = _scale_buffer(N, K, layout, w.device)
+    codes = _empty((N, K), torch.uint8, w.device, stream)
+    scales = _scale_buffer(N, K, layout, w.device, stream)
     with _device(w.device):
         _check(lib().mx_cast_gain_fwd(w.data_ptr(), N, K, gamma.data_ptr(), float(c), codes.data_ptr(),
                                       scales.data_ptr(), SCALE_LAYOUT[layout], _stream_ptr(w.device, stream)))
@@ -429,7 +449,7 @@ def linear_fwd(x_codes, x_scales, inv_rms, w_codes, w_scales, out=None, stream=N
         _require(w_scales, "w_scales", dev, min_numel=mma_scale_bytes(N, K), byte_elems=True)
     _require(inv_rms, "inv_rms", dev, torch.float32, T)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, N), torch.bfloat16, dev, stream)
     _require(out, "out", dev, torch.bfloat16, T * N)
     with _device(dev):
         _check(lib().mxnorm_linear_fwd(x_codes.data_ptr(), x_scales.data_ptr(), inv_rms.data_ptr(),
@@ -454,7 +474,7 @@ def bwd_ste(x, dy, inv_rms, out=None, stream=None):
         raise ValueError("inv_rms needs one value per row")
     _require(dy, "dy", x.device)
     _require(inv_rms, "inv_rms", x.device, torch.float32, T)
-    dx = torch.empty_like(x) if out is None else out
+    dx = _empty(tuple(x.shape), torch.bfloat16, x.device, stream) if out is None else out
     _require(dx, "out", x.device, torch.bfloat16, T * H)
     with _device(x.device):
         _check(lib().mxnorm_bwd_ste(x.data_ptr(), dy.data_ptr(), inv_rms.data_ptr(), T, H, dx.data_ptr(),
@@ -737,7 +757,7 @@ def _wgrad(entry, x_codes, x_scales, inv_rms, dout, layout, out, stream, *drill)
         dw = out
         _need(dw, "out", index, N * K, torch.bfloat16)
     need = lib().mxnorm_linear_wgrad_workspace_bytes(T, K, N)
-    ws = _empty((need,), torch.uint8, dev, stream) if need > 0 else None
+    ws = _workspace((need,), torch.uint8, dev, stream) if need > 0 else None
     _launch(getattr(lib(), entry), dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), lay, _ptr(inv_rms),
             dout.data_ptr(), T, K, N, dw.data_ptr(), _ptr(ws), max(0, need), *drill)
     return dw
@@ -764,9 +784,9 @@ def tiled_wait_drill(x, withheld_tile: int = 0, wait_limit_ns: int = 2_000_000, 
     H = x.shape[-1]
     T = x.numel() // H if H else 0
     if out is None:
-        out = (torch.empty((T, H), dtype=torch.uint8, device=x.device),
-               torch.empty((T, H // 32), dtype=torch.uint8, device=x.device),
-               torch.empty((T,), dtype=torch.float32, device=x.device))
+        out = (_empty((T, H), torch.uint8, x.device, stream),
+               _empty((T, H // 32), torch.uint8, x.device, stream),
+               _empty((T,), torch.float32, x.device, stream))
     codes, scales, inv = out
     _require(codes, "codes", x.device, min_numel=T * H, byte_elems=True)
     _require(scales, "scales", x.device, min_numel=T * (H // 32), byte_elems=True)
