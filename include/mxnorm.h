@@ -365,7 +365,9 @@ int mx_dequant_fwd(const void* codes, const uint8_t* scales, int64_t T, int64_t 
  * rounded to fp32 and then to bf16.  inv_rms NULL stands for ones (a layer
  * without a norm); the tensor scales g_x, g_w (one fp32 each, device memory)
  * are for MXNORM_FMT_NVFP4 and NULL otherwise.  Both operands have the same
- * fmt.  An output feature or a row whose scales hold a NaN is NaN.
+ * fmt.  An output feature or a row whose scales hold a NaN is NaN.  An
+ * inv_rms of +Inf, which the NVFP4 pass gives a row without a nonzero block
+ * scale, counts as 0: the row's outputs are 0.
  *   x_codes   [T, K/2]  16-byte aligned    x_scales  MXNORM_SCALE_MMA, 16-byte aligned
  *   w_codes   [N, K/2]  16-byte aligned    w_scales  MXNORM_SCALE_MMA, 16-byte aligned
  *   inv_rms   f32 [T]                      out       bf16 [T, N], 16-byte aligned
@@ -389,7 +391,8 @@ int mxnorm_linear_fp4_fwd(const void* x_codes, const uint8_t* x_scales, const fl
  *     dx = rho~ dy - rho~^3 x^ (1/H) sum_j dy_j x^_j.
  *   x_codes  E4M3 [T, H], 16-byte aligned; x_scales E8M0 in scale_layout
  *   dy, inv_rms, dx  as mxnorm_bwd_ste
- * H % 32 == 0 (MMA layout: 128).  Errors and stream semantics as
+ * H % 32 == 0 (MMA layout: 128).  An inv_rms of +Inf counts as 0, as in the
+ * FP4 product: the row's dx is 0.  Errors and stream semantics as
  * mxnorm_bwd_ste. */
 int mxnorm_bwd_ste_ckpt(const void* x_codes, const uint8_t* x_scales, int scale_layout, const void* dy,
                         const float* inv_rms, int64_t T, int64_t H, void* dx, void* stream);
@@ -398,7 +401,8 @@ int mxnorm_bwd_ste_ckpt(const void* x_codes, const uint8_t* x_scales, int scale_
  *     dw[n, k] = bf16( sum_t dout[t, n] h[t, k] ),   h[t, k] = RN_bf16(inv_rms[t] x^[t, k]),
  * accumulated in fp32 (h, the layer's normalised input, is the tensor cores'
  * bf16 operand: its rounding is as far off as that of the bf16 result).
- * inv_rms NULL stands for ones.
+ * inv_rms NULL stands for ones; +Inf counts as 0, as in the FP4 product: the
+ * row adds nothing.
  *   x_codes  E4M3 [T, K], 16-byte aligned; x_scales E8M0 in scale_layout
  *   inv_rms  f32 [T]     dout  bf16 [T, N], 16-byte aligned
  *   dw       bf16 [N, K], 16-byte aligned (overwritten)

@@ -648,7 +648,8 @@ def linear_fwd_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt: str = "mx
     sum_k x^[t, k] w^[n, k]) on the tensor cores; scales in the MMA layout.
     x_codes uint8 [T, K/2] (any T from a single token), w_codes uint8
     [N, K/2]; inv_rms float32 [T] or None (ones); the tensor scales are for
-    "nvfp4".  Returns out [T, N] (bf16)."""
+    "nvfp4".  Rows whose inv_rms is +Inf (NVFP4 rows without a value, such as
+    padding) give zeros.  Returns out [T, N] (bf16)."""
     return _linear_fp4("mxnorm_linear_fp4_fwd", x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_tensor_scale,
                        w_tensor_scale, out, stream)
 
@@ -699,8 +700,8 @@ def bwd_ste_ckpt(x_codes, x_scales, dy, inv_rms, layout: str = "row_major", out=
     """bwd_ste from the forward's MXFP8 codes and scales instead of its bf16
     input: dx = r dy - r^3 x^ mean(dy x^).  x_codes uint8 [..., H] and
     x_scales (in `layout`) as quant_fwd / quant_fwd_mma / mx_cast wrote them;
-    dy: contiguous bf16 CUDA tensor like x; inv_rms float32 [...].  Returns
-    dx (bf16, like dy)."""
+    dy: contiguous bf16 CUDA tensor like x; inv_rms float32 [...] (+Inf, a row
+    without a value: its dx is 0).  Returns dx (bf16, like dy)."""
     import torch
     lay = _layout_of(layout)
     dev = dy.device
@@ -730,7 +731,7 @@ def linear_wgrad_ckpt(x_codes, x_scales, inv_rms, dout, layout: str = "mma", out
     """Weight gradient of MXNormLinear from the MXFP8 checkpoint: dw[n, k] =
     bf16(sum_t dout[t, n] * RN_bf16(inv_rms[t] * x^[t, k])).  x_codes uint8
     [T, K] and x_scales (in `layout`) as the forward wrote them; inv_rms
-    float32 [T] or None (ones); dout: contiguous bf16 CUDA tensor [T, N]
+    float32 [T] or None (ones; a row of +Inf adds nothing); dout: contiguous bf16 CUDA tensor [T, N]
     (N % 8 == 0).  A split sum's workspace is allocated per call (torch's
     allocator, on the call's stream).  Returns dw (bf16 [N, K], overwritten)."""
     return _wgrad("mxnorm_linear_wgrad_ckpt", x_codes, x_scales, inv_rms, dout, layout, out, stream)

@@ -356,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int c0 = m.n0 + 128 * half;
       const int cols = min(128, N - c0);
       float r = g;
-      if (inv_rms != nullptr) r = row < T ? __fmul_rn(inv_rms[row], g) : 0.0f;
+      if (inv_rms != nullptr) r = row < T ? __fmul_rn(row_factor(inv_rms[row]), g) : 0.0f;
       uint32_t o[64];
       scale_pack64(*reinterpret_cast<uint32_t(*)[64]>(v), r, o);
       scale_pack64(*reinterpret_cast<uint32_t(*)[64]>(v + 64), r, o + 32);

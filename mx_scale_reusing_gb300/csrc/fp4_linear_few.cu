@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
   } else {
     const float g = NV ? __fmul_rn(*xg, *wg) : 1.0f;
     for (int r = threadIdx.x - 64; r < rows; r += kThreads - 64)
-      alpha[r] = inv_rms ? __fmul_rn(inv_rms[t0 + r], g) : g;
+      alpha[r] = inv_rms ? __fmul_rn(row_factor(inv_rms[t0 + r]), g) : g;
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 64) : "memory");  // the epilogue warps' alphas
     done = wait_warp(acc_full, 0);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     const uint16_t* gr = dy + row * (int64_t)H;
     const uint8_t* sr = scale_row(const_cast<uint8_t*>(scales), row, KB, tiled);
     uint16_t* dr = dx + row * (int64_t)H;
-    const float r = row < T ? inv_rms[row] : 0.0f;
+    const float r = row < T ? row_factor(inv_rms[row]) : 0.0f;
     float dot = 0.0f;
     if constexpr (NCHUNK > 0) {
       Share s[NCHUNK];

@@ -60,3 +60,51 @@ def test_inv_rms_of_other_rows_is_refused(rows):
         fn(r)
     with pytest.raises(ValueError, match="inv_rms"):
         mx.bwd_ste_ckpt(c, s, x, None)
+
+
+@pytest.mark.parametrize("T", [5, 70, 333, 700])
+@pytest.mark.parametrize("p", [1, 2])
+def test_rows_without_a_value_stay_zero_through_a_layer(T, p):
+    """Padding rows, and rows whose every block scale is lost beside the tensor's largest value, get inv_rms = +Inf from
+    the NVFP4 pass.  Forward and both gradients treat them as zeros and every other row as if they were not there."""
+    K, N = 512, 264
+    torch.manual_seed(T)
+    x = torch.randn((T, K), device="cuda").to(torch.bfloat16)
+    dead = torch.zeros(T, dtype=torch.bool, device="cuda")
+    dead[[0, T // 2, T - 1]] = True
+    x[0] = 0
+    x[T - 1] = 0
+    x[T // 2] *= 2.0 ** -30
+    w = (torch.randn((N, K), device="cuda") * 0.05).to(torch.bfloat16)
+    dout, dh = torch.randn((T, N), device="cuda").to(torch.bfloat16), torch.randn((T, K), device="cuda").to(torch.bfloat16)
+    xc, xs, inv, xg = mx.quant_fwd_nvfp4_mma(x, p)
+    assert torch.equal(torch.isinf(inv), dead)
+    wc, ws, wg = mx.mx_cast_fp4(w, "nvfp4")
+    kc, ks = mx.mx_cast(x, "mma")
+    got = (mx.linear_fwd_fp4(xc, xs, inv, wc, ws, "nvfp4", xg, wg), mx.bwd_ste_ckpt(kc, ks, dh, inv, "mma"),
+           mx.linear_wgrad_ckpt(kc, ks, inv, dout))
+    zeroed = torch.where(dead, torch.zeros_like(inv), inv)
+    want = (mx.linear_fwd_fp4(xc, xs, zeroed, wc, ws, "nvfp4", xg, wg), mx.bwd_ste_ckpt(kc, ks, dh, zeroed, "mma"),
+            mx.linear_wgrad_ckpt(kc, ks, zeroed, dout))
+    for a, b in zip(got, want):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+    assert (got[0][dead] == 0).all() and (got[1][dead] == 0).all()
+    # dW against its formula over the rows that are there: the bound of a sum of T products in fp32, rounded once
+    live = ~dead
+    h = (mx.mx_dequant(kc, ks, layout="mma").float()[live] * inv[live][:, None]).to(torch.bfloat16).double()
+    g = dout[live].double()
+    ref, size = g.t() @ h, g.abs().t() @ h.abs()
+    assert ((got[2].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2 * (T + 8) * 2.0 ** -24 * size * 1.01 + 1e-38).all()
+
+
+@pytest.mark.parametrize("T", [1, 333])
+def test_nan_rows_are_not_taken_for_empty_ones(T):
+    x = torch.randn((T, 256), device="cuda").to(torch.bfloat16)
+    x[T - 1, 7] = float("nan")
+    w = torch.randn((64, 256), device="cuda").to(torch.bfloat16)
+    xc, xs, inv, xg = mx.quant_fwd_nvfp4_mma(x)
+    wc, ws, wg = mx.mx_cast_fp4(w, "nvfp4")
+    kc, ks = mx.mx_cast(x, "mma")
+    assert mx.linear_fwd_fp4(xc, xs, inv, wc, ws, "nvfp4", xg, wg)[T - 1].isnan().all()
+    assert mx.bwd_ste_ckpt(kc, ks, x, inv, "mma")[T - 1].isnan().all()
+    assert mx.linear_wgrad_ckpt(kc, ks, inv, w.new_ones((T, 64))).isnan().all()
