@@ -352,9 +352,12 @@ int mxnorm_absmax_gain_bf16(const void* w, int64_t N, int64_t K, const float* ga
 /* Quantised rows read back: out[t, j] = bf16(code * block scale), for
  * MXNORM_FMT_NVFP4 bf16(RN_fp32(code * block scale * tensor scale)) (code
  * times block scale is exact in fp32).  Exact for the MX formats within the
- * bf16 range.  Rotated formats give the rotated values.  Blocks with a NaN
- * scale give NaN.  fmt: any mxnorm_fmt; scales in scale_layout; tensor_scale
- * as mx_cast_fp4_fwd.  codes, out (bf16 [T, H]): 16-byte aligned. */
+ * bf16 range.  Rotated formats give the rotated values: a gradient through a
+ * rotated weight is in the rotated basis until each group of 16 or 32 is
+ * rotated once more (the rotation is its own inverse).  Blocks with a NaN
+ * scale give NaN.  fmt: any mxnorm_fmt; scales in scale_layout; tensor_scale:
+ * the cast's, one fp32 in device memory for NVFP4 (not checked), else NULL.
+ * codes, out (bf16 [T, H]): 16-byte aligned. */
 int mx_dequant_fwd(const void* codes, const uint8_t* scales, int64_t T, int64_t H, int fmt, int scale_layout,
                    const float* tensor_scale, void* out, void* stream);
 

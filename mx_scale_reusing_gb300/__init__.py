@@ -619,7 +619,10 @@ def quant_fwd_nvfp4_mma(x, p: int = 2, tensor_scale=None, stream=None):
 def mx_dequant(codes, scales, fmt: str = "mxfp8", layout: str = "row_major", tensor_scale=None, out=None,
                stream=None):
     """The bf16 values that codes [..., H or H/2] and their block scales stand
-    for (rotated formats: the rotated values).  Row-major scales end in the
+    for.  Rotated formats give the rotated values: each aligned group of 16 or
+    32 times the orthonormal Hadamard matrix in Sylvester order, its own
+    inverse, so a gradient through a rotated weight, dout @ out, takes the
+    matrix once more to leave the rotated basis.  Row-major scales end in the
     row's blocks, [..., H/32 or H/16]; the MMA layout is flat.  "nvfp4" takes the cast's
     tensor scale (1-element float32 CUDA tensor).  Returns bf16 [..., H]."""
     import torch

@@ -52,3 +52,53 @@ def test_dw_hand_over_between_the_ctas_of_a_pair(T, K, N):
     bound = 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * 2 * (T + 8) * U * size + 1e-38
     assert ((outs[0].double() - want).abs() <= bound).all()
     assert mx.device_errors() == 0
+
+
+def hadamard_matrix(n):
+    """Orthonormal, Sylvester order: entry (i, j) has the sign of the parity of i & j."""
+    i = torch.arange(n)
+    bits = (i[:, None] & i[None, :])
+    parity = sum((bits >> k) & 1 for k in range(5)) % 2
+    return ((1 - 2 * parity).double() / n ** 0.5).cuda()
+
+
+@pytest.mark.parametrize("fmt,n", [("mxfp4_h16", 16), ("mxfp4_h32", 32)])
+def test_training_step_of_a_rotated_layer(fmt, n):
+    """The weight that a rotated product used reads back rotated.  dh of the layer's (unrotated) normalised input is
+    dout @ w_used rotated once more: against central differences in 64 bits of sum(dout * (h H) w_used^T), which is
+    linear in h.  It then goes into dx beside unrotated codes."""
+    T, K, N = 70, 256, 136
+    x, w = dev(synth.make_random_rows(T, K, 1, 2.0)), dev(synth.make_random_rows(N, K, 2, 0.05))
+    gb = synth.make_random_rows(T, N, 3, 0.1)
+    dout = dev(gb)
+    xc, xs, inv = mx.quant_fwd_mma(x, fmt=fmt)
+    wc, ws, _ = mx.mx_cast_fp4(w, fmt)
+    out = mx.linear_fwd_fp4(xc, xs, inv, wc, ws, fmt)
+    w_used, Hn = mx.mx_dequant(wc, ws, fmt, "mma"), hadamard_matrix(n)
+
+    def rotated(v):
+        return (v.unflatten(1, (-1, n)) @ Hn).flatten(1)
+
+    # the forward multiplied these: rotated rows by rotated rows
+    xr = mx.mx_dequant(xc, xs, fmt, "mma").double()
+    want = inv.double()[:, None] * (xr @ w_used.double().t())
+    size = inv.double()[:, None] * (xr.abs() @ w_used.double().abs().t())
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2 * K * U * size + 3 * U * want.abs()) * 1.01).all()
+    # rotating twice is nothing, and the rotated cast of x approximates x rotated
+    assert torch.allclose(rotated(rotated(x.double())), x.double(), rtol=0, atol=1e-9)
+    assert torch.nn.functional.cosine_similarity(rotated(xr).flatten(), x.double().flatten(), dim=0) > 0.95
+    dh = rotated(dout.double() @ w_used.double())
+    h0, g = torch.randn((T, K), dtype=torch.float64, device="cuda"), dout.double()
+    for j in range(0, K, 37):
+        e = torch.zeros_like(h0)
+        e[:, j] = 0.5
+        up, down = ((g * (rotated(h0 + s * e) @ w_used.double().t())).sum(1) for s in (1, -1))
+        assert torch.allclose(up - down, dh[:, j], rtol=1e-9, atol=1e-9)
+    kc, ks, r = mx.quant_fwd_mma(x)   # the checkpoint: unrotated codes, with their own inverse RMS
+    dhb = dh.to(torch.bfloat16)
+    dx = mx.bwd_ste_ckpt(kc, ks, dhb, r, "mma").double()
+    xv, d, rr = mx.mx_dequant(kc, ks, layout="mma").double(), dhb.double(), r.double()[:, None]
+    exact = rr * d - rr ** 3 * xv * (d * xv).mean(1, keepdim=True)
+    size = rr * d.abs() + rr ** 3 * xv.abs() * (d * xv).abs().mean(1, keepdim=True)
+    # bf16 output; fp32 steps, each within u of its term: a dozen for the sum's tree, six around it
+    assert ((dx - exact).abs() <= 2.0 ** -8 * exact.abs() + 20 * U * size).all()
