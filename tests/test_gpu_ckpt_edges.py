@@ -102,3 +102,23 @@ def test_training_step_of_a_rotated_layer(fmt, n):
     size = rr * d.abs() + rr ** 3 * xv.abs() * (d * xv).abs().mean(1, keepdim=True)
     # bf16 output; fp32 steps, each within u of its term: a dozen for the sum's tree, six around it
     assert ((dx - exact).abs() <= 2.0 ** -8 * exact.abs() + 20 * U * size).all()
+
+
+@pytest.mark.parametrize("T,K,N,layout", [(1, 32, 8, "row_major"), (100, 416, 264, "row_major"), (700, 256, 136, "mma"),
+                                          (2043, 768, 768, "mma"), (20000, 64, 72, "row_major")])
+def test_dw_whole_rounding_error(T, K, N, layout):
+    """dW against dout^T (r x^) in 64 bits, with nothing rounded before the sum.  The operand h = r x^ rounds to bf16 (half
+    a step: 2^-8 of each term, after two fp32 roundings), products and sums as in fp32, the result 2^-8:
+      |dw - exact| <= 2^-8 |exact| + (1 + 2^-8) (2^-8 + 3 u + 2 (T + 8) u (1 + 2^-8)) S,  S = sum |dout r x^|.
+    The roundings of h are as good as independent, so that over the matrix they add in squares: the 2-norm of the error is
+    within 2^-8 of ||exact|| + ||sqrt(sum (dout r x^)^2)||, the accumulation's share aside."""
+    x, dout = dev(synth.make_random_rows(T, K, T, 2.0)), dev(synth.make_random_rows(T, N, T + 1, 0.05))
+    c, s, inv = mx.quant_fwd(x) if layout == "row_major" else mx.quant_fwd_mma(x)
+    dw = mx.linear_wgrad_ckpt(c, s, inv, dout, layout).double()
+    h, g = mx.mx_dequant(c, s, layout=layout).double() * inv.double()[:, None], dout.double()
+    exact, size = g.t() @ h, g.abs().t() @ h.abs()
+    err = (dw - exact).abs()
+    r = 2.0 ** -8
+    assert (err <= r * exact.abs() + (1 + r) * (r + 3 * U + 2 * (T + 8) * U * (1 + r)) * size + 1e-38).all()
+    squares = ((g * g).t() @ (h * h)).sum().sqrt()
+    assert err.norm() <= r * (exact.norm() + squares) + 2 * (T + 8) * U * size.norm()
