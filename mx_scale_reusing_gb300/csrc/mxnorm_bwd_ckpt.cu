@@ -127,6 +127,17 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
+// A row whose r is +Inf (row_factor) gets zeros.  A branch of its own: taking r
+// as 0 from the start held the next row's loads back (65536 x 4096: 214 us, 204
+// so).
+template <int LANES>
+__device__ __noinline__ void zero_row(uint16_t* dr, int t, int Hr) {
+  for (int e0 = t * 16; e0 < Hr; e0 += LANES * 16) {
+    stg16(dr + e0, 0u, 0u, 0u, 0u);
+    stg16(dr + e0 + 8, 0u, 0u, 0u, 0u);
+  }
+}
+
 // LANES: threads that share a row (8 or 16: several rows a warp; 32; or a
 // whole CTA).  NCHUNK > 0: rows of at most NCHUNK chunks of LANES x 16
 // elements, held in registers; NCHUNK == 0: any H, two passes over the row.
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     const uint16_t* gr = dy + row * (int64_t)H;
     const uint8_t* sr = scale_row(const_cast<uint8_t*>(scales), row, KB, tiled);
     uint16_t* dr = dx + row * (int64_t)H;
-    const float r = row < T ? row_factor(inv_rms[row]) : 0.0f;
+    const float r = row < T ? inv_rms[row] : 0.0f;
     float dot = 0.0f;
     if constexpr (NCHUNK > 0) {
       Share s[NCHUNK];
@@ -171,6 +182,10 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       for (int c = 0; c < NCHUNK; ++c)
         if (c * kStep + t * 16 < Hr) dot = __fadd_rn(dot, share_dot(s[c], r));
       const float m = __fdiv_rn(row_sum<LANES>(dot, red[turn]), (float)H);
+      if (empty_row(r)) {
+        zero_row<LANES>(dr, t, Hr);
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < NCHUNK; ++c) {
         const int e0 = c * kStep + t * 16;
@@ -190,6 +205,10 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
           if ((c0 + b) * kStep + t * 16 < Hr) dot = __fadd_rn(dot, share_dot(s[b], r));
       }
       const float m = __fdiv_rn(row_sum<LANES>(dot, red[turn]), (float)H);
+      if (empty_row(r)) {
+        zero_row<LANES>(dr, t, Hr);
+        continue;
+      }
       for (int c0 = 0; c0 * kStep < H; c0 += B) {
 #pragma unroll
         for (int b = 0; b < B; ++b) {

@@ -384,15 +384,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (row[j] < rows) e[j] = __ldg(base + at[j]);
         }
         float r0 = 0.0f, r1 = 0.0f;  // rows past T: h = 0
-        if (lane < rows) r0 = inv_rms != nullptr ? row_factor(__ldg(inv_rms + (int64_t)st * kBT + lane)) : 1.0f;
-        if (lane + 32 < rows) r1 = inv_rms != nullptr ? row_factor(__ldg(inv_rms + (int64_t)st * kBT + lane + 32)) : 1.0f;
+        if (lane < rows) r0 = inv_rms != nullptr ? __ldg(inv_rms + (int64_t)st * kBT + lane) : 1.0f;
+        if (lane + 32 < rows) r1 = inv_rms != nullptr ? __ldg(inv_rms + (int64_t)st * kBT + lane + 32) : 1.0f;
         if (!q.first && !(ok = wait_warp(c_empty0 + 8 * q.s, q.phase ^ 1u))) break;
         float* dst = sP + q.s * (kStageP / 4);
 #pragma unroll
         for (int j = 0; j < 2 * kMaxG; ++j)
           if (j < 2 * G) dst[lane + 32 * j] = e8m0_value(e[j]);
-        dst[kBT * kMaxG + lane] = r0;
-        dst[kBT * kMaxG + lane + 32] = r1;
+        dst[kBT * kMaxG + lane] = row_factor(r0);  // here, where the loads need to have ended anyway
+        dst[kBT * kMaxG + lane + 32] = row_factor(r1);
         __syncwarp();
         if (lane == 0)
           asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_full0 + 8 * q.s) : "memory");

@@ -35,9 +35,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // block scales are all 0 (padding, or values lost beside the tensor's largest):
 // the forward multiplied zeros there, so the row counts as 0 and not as the NaN
 // of 0 times Inf, which a single padded row would carry into all of dW.
-__device__ __forceinline__ float row_factor(float inv_rms) {
-  return inv_rms == __uint_as_float(0x7F800000u) ? 0.0f : inv_rms;
-}
+__device__ __forceinline__ bool empty_row(float inv_rms) { return inv_rms == __uint_as_float(0x7F800000u); }
+__device__ __forceinline__ float row_factor(float inv_rms) { return empty_row(inv_rms) ? 0.0f : inv_rms; }
 // Value of an E8M0 scale byte: 2^(b - 127) (b = 0: the subnormal 2^-127; 0xFF: NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t b) {
   return b == 0u ? 0x1p-127f : __uint_as_float(b == 0xFFu ? 0x7FC00000u : b << 23);
