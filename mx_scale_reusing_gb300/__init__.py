@@ -184,11 +184,12 @@ def _empty(shape, dtype, device, stream):
     the output once it has waited for `stream`, and the memory is not used
     again before both are done with it."""
     import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     t = _workspace(shape, dtype, device, stream)
-    if stream is not None:
-        current = torch.cuda.current_stream(device)
-        if current != stream:
-            t.record_stream(current)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
     return t
 
 
@@ -528,13 +529,9 @@ def _need_scales(t, name, index, rows, H, fmt, layout):
     _need(t, name, index, _scale_bytes(rows, H, fmt, layout))
 
 
-def _need_inv_rms(t, index, rows):
-    """_need for the rows' factors, one a row, where they are given."""
-    import torch
-    if t is not None:
-        _need(t, "inv_rms", index, rows, torch.float32)
-        if t.numel() != rows:
-            raise ValueError(f"inv_rms holds {t.numel()} values for {rows} rows")
+def _one_a_row(inv_rms, rows):
+    if inv_rms.numel() != rows:
+        raise ValueError(f"inv_rms holds {inv_rms.numel()} values for {rows} rows")
 
 
 def _fp4_out(rows, K, fmt, layout, device, out, stream):
@@ -646,19 +643,13 @@ def mx_dequant(codes, scales, fmt: str = "mxfp8", layout: str = "row_major", ten
 
 
 def linear_fwd_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt: str = "mxfp4", x_tensor_scale=None,
-                   w_tensor_scale=None, out=None, stream=None):
+                   w_tensor_scale=None, out=None, stream=None, *, _drill=()):
     """MXNormLinear's product on FP4 codes: out = bf16(inv_rms[t] * g_x * g_w *
     sum_k x^[t, k] w^[n, k]) on the tensor cores; scales in the MMA layout.
     x_codes uint8 [T, K/2] (any T from a single token), w_codes uint8
     [N, K/2]; inv_rms float32 [T] or None (ones); the tensor scales are for
     "nvfp4".  Rows whose inv_rms is +Inf (NVFP4 rows without a value, such as
     padding) give zeros.  Returns out [T, N] (bf16)."""
-    return _linear_fp4("mxnorm_linear_fp4_fwd", x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_tensor_scale,
-                       w_tensor_scale, out, stream)
-
-
-def _linear_fp4(entry, x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_tensor_scale, w_tensor_scale, out, stream,
-                *drill):
     import torch
     f = _fmt_of(FP4_FMT, fmt)
     if getattr(x_codes, "dim", lambda: 0)() != 2 or getattr(w_codes, "dim", lambda: 0)() != 2:
@@ -673,7 +664,9 @@ def _linear_fp4(entry, x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_ten
     _need(w_codes, "w_codes", index, 0)
     _need_scales(x_scales, "x_scales", index, T, K, fmt, "mma")
     _need_scales(w_scales, "w_scales", index, N, K, fmt, "mma")
-    _need_inv_rms(inv_rms, index, T)
+    if inv_rms is not None:
+        _need(inv_rms, "inv_rms", index, T, torch.float32)
+        _one_a_row(inv_rms, T)
     if x_tensor_scale is not None:
         _need(x_tensor_scale, "x_tensor_scale", index, 1, torch.float32)
     if w_tensor_scale is not None:
@@ -682,9 +675,9 @@ def _linear_fp4(entry, x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_ten
         out = _empty((T, N), torch.bfloat16, dev, stream)
     else:
         _need(out, "out", index, T * N, torch.bfloat16)
-    _launch(getattr(lib(), entry), dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), _ptr(inv_rms),
-            w_codes.data_ptr(), w_scales.data_ptr(), T, K, N, f, _ptr(x_tensor_scale), _ptr(w_tensor_scale),
-            out.data_ptr(), *drill)
+    fn = lib().mxnorm_linear_fp4_wait_drill if _drill else lib().mxnorm_linear_fp4_fwd
+    _launch(fn, dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), _ptr(inv_rms), w_codes.data_ptr(),
+            w_scales.data_ptr(), T, K, N, f, _ptr(x_tensor_scale), _ptr(w_tensor_scale), out.data_ptr(), *_drill)
     return out
 
 
@@ -694,8 +687,8 @@ def linear_fp4_wait_drill(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt: st
     """Failure-detection drill (mxnorm_linear_fp4_wait_drill): the FP4 product
     with the loads of one stage withheld, so that its bounded waits expire
     and bit 3 of device_errors is set.  Returns out, whose values are invalid."""
-    return _linear_fp4("mxnorm_linear_fp4_wait_drill", x_codes, x_scales, inv_rms, w_codes, w_scales, fmt,
-                       x_tensor_scale, w_tensor_scale, out, stream, int(withheld_stage), int(wait_limit_ns))
+    return linear_fwd_fp4(x_codes, x_scales, inv_rms, w_codes, w_scales, fmt, x_tensor_scale, w_tensor_scale, out,
+                          stream, _drill=(int(withheld_stage), int(wait_limit_ns)))
 
 
 # -------------------------------------------------------- 8-bit checkpoints
@@ -717,9 +710,8 @@ def bwd_ste_ckpt(x_codes, x_scales, dy, inv_rms, layout: str = "row_major", out=
     T = dy.numel() // H if H else 0
     _need(x_codes, "x_codes", index, 0)
     _need_scales(x_scales, "x_scales", index, T, H, "mxfp8", layout)
-    if inv_rms is None:
-        raise ValueError("inv_rms must be a contiguous CUDA tensor")
-    _need_inv_rms(inv_rms, index, T)
+    _need(inv_rms, "inv_rms", index, T, torch.float32)
+    _one_a_row(inv_rms, T)
     if out is None:
         dx = _empty(shape, torch.bfloat16, dev, stream)
     else:
@@ -730,17 +722,14 @@ def bwd_ste_ckpt(x_codes, x_scales, dy, inv_rms, layout: str = "row_major", out=
     return dx
 
 
-def linear_wgrad_ckpt(x_codes, x_scales, inv_rms, dout, layout: str = "mma", out=None, stream=None):
+def linear_wgrad_ckpt(x_codes, x_scales, inv_rms, dout, layout: str = "mma", out=None, stream=None, *, _drill=()):
     """Weight gradient of MXNormLinear from the MXFP8 checkpoint: dw[n, k] =
     bf16(sum_t dout[t, n] * RN_bf16(inv_rms[t] * x^[t, k])).  x_codes uint8
     [T, K] and x_scales (in `layout`) as the forward wrote them; inv_rms
-    float32 [T] or None (ones; a row of +Inf adds nothing); dout: contiguous bf16 CUDA tensor [T, N]
-    (N % 8 == 0).  A split sum's workspace is allocated per call (torch's
-    allocator, on the call's stream).  Returns dw (bf16 [N, K], overwritten)."""
-    return _wgrad("mxnorm_linear_wgrad_ckpt", x_codes, x_scales, inv_rms, dout, layout, out, stream)
-
-
-def _wgrad(entry, x_codes, x_scales, inv_rms, dout, layout, out, stream, *drill):
+    float32 [T] or None (ones; a row of +Inf adds nothing); dout: contiguous
+    bf16 CUDA tensor [T, N] (N % 8 == 0).  A split sum's workspace is allocated
+    per call (torch's allocator, on the call's stream).  Returns dw (bf16
+    [N, K], overwritten)."""
     import torch
     lay = _layout_of(layout)
     if getattr(x_codes, "dim", lambda: 0)() != 2 or getattr(dout, "dim", lambda: 0)() != 2:
@@ -754,7 +743,9 @@ def _wgrad(entry, x_codes, x_scales, inv_rms, dout, layout, out, stream, *drill)
     _need(x_codes, "x_codes", index, 0)
     _need_scales(x_scales, "x_scales", index, T, K, "mxfp8", layout)
     _need(dout, "dout", index, 0, torch.bfloat16)
-    _need_inv_rms(inv_rms, index, T)
+    if inv_rms is not None:
+        _need(inv_rms, "inv_rms", index, T, torch.float32)
+        _one_a_row(inv_rms, T)
     if out is None:
         dw = _empty((N, K), torch.bfloat16, dev, stream)
     else:
@@ -762,8 +753,9 @@ def _wgrad(entry, x_codes, x_scales, inv_rms, dout, layout, out, stream, *drill)
         _need(dw, "out", index, N * K, torch.bfloat16)
     need = lib().mxnorm_linear_wgrad_workspace_bytes(T, K, N)
     ws = _workspace((need,), torch.uint8, dev, stream) if need > 0 else None
-    _launch(getattr(lib(), entry), dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), lay, _ptr(inv_rms),
-            dout.data_ptr(), T, K, N, dw.data_ptr(), _ptr(ws), max(0, need), *drill)
+    fn = lib().mxnorm_linear_wgrad_wait_drill if _drill else lib().mxnorm_linear_wgrad_ckpt
+    _launch(fn, dev, stream, x_codes.data_ptr(), x_scales.data_ptr(), lay, _ptr(inv_rms), dout.data_ptr(),
+            T, K, N, dw.data_ptr(), _ptr(ws), max(0, need), *_drill)
     return dw
 
 
@@ -773,8 +765,8 @@ def linear_wgrad_wait_drill(x_codes, x_scales, inv_rms, dout, layout: str = "mma
     gradient with one load of its pipeline withheld (0: dout's, 1: the
     codes', of the given stage), so that its bounded waits expire and bit 4
     of device_errors is set.  Returns dw, whose values are invalid."""
-    return _wgrad("mxnorm_linear_wgrad_wait_drill", x_codes, x_scales, inv_rms, dout, layout, out, stream,
-                  int(withheld_load), int(withheld_stage), int(wait_limit_ns))
+    return linear_wgrad_ckpt(x_codes, x_scales, inv_rms, dout, layout, out, stream,
+                             _drill=(int(withheld_load), int(withheld_stage), int(wait_limit_ns)))
 
 
 def tiled_wait_drill(x, withheld_tile: int = 0, wait_limit_ns: int = 2_000_000, out=None, stream=None):
