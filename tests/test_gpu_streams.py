@@ -101,3 +101,21 @@ def test_a_stream_that_only_names_its_handle(d):
     outs = mx.quant_fwd(d["x"], stream=Handle(side))
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, (d["c"], d["s"], d["inv"])))
+
+
+def test_stream_argument_in_a_capture(d):
+    """A fork of the captured stream: the calls' memory is the graph's, whichever stream they name."""
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    want = mx.linear_wgrad_ckpt(*mx.quant_fwd(d["x"]), d["dout"], "row_major")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        current = torch.cuda.current_stream()
+        side.wait_stream(current)
+        for _ in range(3):   # outputs dropped and taken again within the capture
+            got = mx.linear_wgrad_ckpt(*mx.quant_fwd(d["x"], stream=side), d["dout"], "row_major", stream=side)
+        current.wait_stream(side)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
