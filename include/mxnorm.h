@@ -403,7 +403,8 @@ int mxnorm_bwd_ste_ckpt(const void* x_codes, const uint8_t* x_scales, int scale_
 /* Weight gradient of MXNormLinear,
  *     dw[n, k] = bf16( sum_t dout[t, n] h[t, k] ),   h[t, k] = RN_bf16(inv_rms[t] x^[t, k]),
  * accumulated in fp32 (h, the layer's normalised input, is the tensor cores'
- * bf16 operand: its rounding is as far off as that of the bf16 result).
+ * bf16 operand: its rounding is as far off as that of the bf16 result, so dw is
+ * about sqrt(2) times as far from the unrounded sum as its own rounding).
  * inv_rms NULL stands for ones; +Inf counts as 0, as in the FP4 product: the
  * row adds nothing.
  *   x_codes  E4M3 [T, K], 16-byte aligned; x_scales E8M0 in scale_layout

@@ -30,13 +30,17 @@
 // zero scales add nothing.  Every mbarrier wait is bounded (2 s); on expiry
 // bit 0 of the error word is set and the pair winds down after its own copies
 // and MMAs.
-// What bounds it: shared memory's 128 bytes a clock.  A stage writes 38 KB
-// (NVFP4) and its MMAs and scale copies read 38 KB in 512 clocks of tensor
-// time, some 600 clocks of shared memory; 656 are measured, and some 1000
-// more a tile to hand the accumulators over (TMEM has no room for a second
-// set beside the scales).  65536 x 4096 x 4096: 325 to 345 us, 6400 to 6800
-// TFLOP/s; without the output's stores 286 us, without scale copies 300.
-// Swapping pieces between lanes so that a store fills whole lines was slower
+// 65536 x 4096 x 4096, replayed from a graph: NVFP4 332 to 350 us, 6300 to
+// 6600 TFLOP/s, MXFP4 324 to 338; single calls 366 to 380 us.  A library's
+// NVFP4 product takes 300 us on the same chip, so what follows is where the
+// time goes and no floor.  A stage writes 38 KB (NVFP4) and its MMAs and scale
+// copies read 38 KB, some 600 clocks of shared memory's 128 bytes a clock
+// beside 512 of tensor time; 656 are measured.  Some 1000 more a tile pass
+// while the accumulators are handed over: a second set (256 more columns) has
+// no room in TMEM beside any scales, half a set would have with two or three
+// scale slots instead of the ring's five.  Neither that nor instructions of
+// K = 96 is built, so neither is timed.  Of 332 us, leaving out the output's
+// stores gave 286 and leaving out the scale copies 300.  Swapping pieces between lanes so that a store fills whole lines was slower
 // (4096 x 4096 x 4096: 30.7 us against 29.5).
 #include <algorithm>
 

@@ -28,8 +28,10 @@
 // Two accumulators (512 features) share a stage's h where there are features
 // enough: made once for twice the MMAs, h stops bounding the loop (by the
 // bandwidth of shared memory: dout in, h in, both out to the MMA).  16384 x
-// 4096 x 4096: 303 us, 1813 TFLOP/s, 97 % of the measured bf16 rate of a
-// library product (285 us on h expanded beforehand); one accumulator 447 us.
+// 4096 x 4096, replayed from a graph: 303 to 307 us, 1800 TFLOP/s, 96 % of the
+// measured bf16 rate of a library product (1872 TFLOP/s in a short burst) and
+// 93 % of that product at this size (285 us, on h expanded beforehand); single
+// calls 335 to 340 us; one accumulator 447 us.
 // Narrow tiles of one are bound by the MMA chain (some 115 clocks each).
 // Where tiles are few, the rows are split over S pairs a tile: fp32 partial
 // sums go to the caller's workspace [S][N][K] and a second kernel adds them in
@@ -627,8 +629,11 @@ double stage_clocks(int MT, int W) {
 // is HBM's (65536 x 4096 x 4096: 1270 us whole, 1310 in four parts of rows).
 // 3000 of the join's constant are measured; 6000 stand for its launch and
 // workspace, which an eager caller waits for where the kernel is short (2043 x
-// 768 x 768: 14.0 us whole and 11.4 in four parts on the device, but 14 and 18
-// a call of the host's time; 4096 x 1024 x 1024: 27 whole, 17 in four).
+// 768 x 768: 14.6 us whole and 11.7 in four parts on the device, but 14 and 18
+// a call of the host's time; 4096 x 1024 x 1024: 27 whole, 17 in four).  So a
+// caller that replays a graph is off the best plan by up to 25 % there, 14 % at
+// 2048 x 2048 x 512 and 12 % at 30001 x 416 x 264; at the other 14 sizes swept
+// by 10 % at most, at 11 of them by 1 %.
 Plan search(int64_t T, int64_t K, int64_t N) {
   const int64_t stages = (T + kBT - 1) / kBT;
   Plan best{1, kMaxW, 1};
