@@ -122,3 +122,24 @@ def test_dw_whole_rounding_error(T, K, N, layout):
     assert (err <= r * exact.abs() + (1 + r) * (r + 3 * U + 2 * (T + 8) * U * (1 + r)) * size + 1e-38).all()
     squares = ((g * g).t() @ (h * h)).sum().sqrt()
     assert err.norm() <= r * (exact.norm() + squares) + 2 * (T + 8) * U * size.norm()
+
+
+@pytest.mark.parametrize("T,H,layout", [(70, 32, "row_major"), (70, 128, "mma"), (71, 224, "row_major"), (70, 512, "mma"), (2000, 1024, "mma"),
+                                        (70, 1024, "mma"), (5000, 2048, "mma"), (70, 4096, "mma"), (5000, 4096, "row_major"),
+                                        (9, 8192, "mma"), (5, 16384, "mma"), (5, 16416, "row_major")])
+def test_dx_of_rows_without_a_value(T, H, layout):
+    """inv_rms = +Inf gives dx = 0 in every form of the kernel (several rows a warp, a warp, a CTA a row, rows read twice),
+    NaN stays NaN, and the other rows keep the bits that they have without such neighbours."""
+    x, dy = dev(synth.make_random_rows(T, H, 1, 2.0)), dev(synth.make_random_rows(T, H, 2))
+    c, s, inv = mx.quant_fwd(x) if layout == "row_major" else mx.quant_fwd_mma(x)
+    want = mx.bwd_ste_ckpt(c, s, dy, inv, layout)
+    empty, bad = torch.zeros(T, dtype=torch.bool, device="cuda"), torch.zeros(T, dtype=torch.bool, device="cuda")
+    empty[0::3] = True
+    bad[1::7] = True
+    bad &= ~empty
+    r = inv.clone()
+    r[empty], r[bad] = float("inf"), float("nan")
+    got = mx.bwd_ste_ckpt(c, s, dy, r, layout)
+    assert (got[empty] == 0).all() and got[bad].isnan().all()
+    rest = ~(empty | bad)
+    assert torch.equal(got[rest], want[rest])
