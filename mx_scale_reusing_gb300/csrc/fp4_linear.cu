@@ -40,8 +40,9 @@
 // no room in TMEM beside any scales, half a set would have with two or three
 // scale slots instead of the ring's five.  Neither that nor instructions of
 // K = 96 is built, so neither is timed.  Of 332 us, leaving out the output's
-// stores gave 286 and leaving out the scale copies 300.  Swapping pieces between lanes so that a store fills whole lines was slower
-// (4096 x 4096 x 4096: 30.7 us against 29.5).
+// stores gave 286 and leaving out the scale copies 300.  Swapping pieces
+// between lanes so that a store fills whole lines was slower (4096 x 4096 x
+// 4096: 30.7 us against 29.5).
 #include <algorithm>
 
 #include "fp4_tc.cuh"
